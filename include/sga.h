@@ -204,6 +204,107 @@ SGA_API sga_status_t sga_forward_fused_fp8(const sga_dims_t* dims, const sga_fp8
                                            int32_t* idx_out, float* out, void* ws, size_t ws_bytes,
                                            sga_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The latent cache in 4 bits (arXiv abstract "A.X K2 Technical Report": the
+ * model is served in NVFP4; archdb "A.X K2", KV fields: 512 latent + 64 rope
+ * values per token).  A cache row is SGA_KV4_ROW_BYTES bytes, [B][L][416]
+ * (16-byte aligned):
+ *   bytes   0..255  512 E2M1 codes (1 sign, 2 exponent, 1 mantissa bit:
+ *                   +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}); byte j holds latent dim 2j
+ *                   in its low half and dim 2j+1 in its high half
+ *   bytes 256..287  32 E4M3 scales, byte 256+g for latent dims 16g .. 16g+15
+ *   bytes 288..415  the 64 rope values, bf16
+ * Latent dim d stands for code * scale, which is exact in bf16.  A row takes
+ * 0.36 of the 1,152 bytes of a bf16 row. */
+#define SGA_KV4_ROW_BYTES 416
+
+/* Writes rows into the 4-bit cache: kv4[b, q_pos[b,i]] = quantised
+ * kv_rows[b,i] for every (b, i); no other row is touched.
+ *   kv_rows [B][T][576] bf16    q_pos [B][T] int32    kv4 [B][L][416] bytes
+ * For each group of 16 latent dims the scale is the E4M3 value nearest to
+ * max|x| / 6 (at most 448), each code the E2M1 value nearest to x / scale, ties
+ * to the even code, at most 6 in magnitude.  So groups whose largest value
+ * is above 2,688 saturate, and those below 6 * 2^-10 become zeros.  A group
+ * with a NaN gets a NaN scale (all 16 values read as NaN).  The positions of
+ * one sequence must be distinct.  dims->top_k is not used.  Workspace: the
+ * status word only, 256 bytes.  Device error: a position outside [0, L) (that
+ * row is skipped). */
+SGA_API sga_status_t sga_kv4_append(const sga_dims_t* dims, const sga_bf16_t* kv_rows, const int32_t* q_pos,
+                                    uint8_t* kv4, void* ws, size_t ws_bytes, sga_stream_t stream);
+
+/* Reads rows of the 4-bit cache: kv_rows[b,i] = the 576 values of
+ * kv4[b, pos[b,i]] (exact in bf16), zeros where pos[b,i] = -1.  Shapes as for
+ * sga_kv4_append; positions may repeat.  Workspace: 256 bytes.  Device error:
+ * a position outside [-1, L) (zeros are written). */
+SGA_API sga_status_t sga_kv4_read(const sga_dims_t* dims, const uint8_t* kv4, const int32_t* pos,
+                                  sga_bf16_t* kv_rows, void* ws, size_t ws_bytes, sga_stream_t stream);
+
+/* sga_sparse_mla_attend over the 4-bit cache: the same formulas on the rows'
+ * values, with the output rounded to bf16 (the type the next projection
+ * reads).
+ *   q    [B][T][64][576] bf16        kv4 [B][L][416] bytes
+ *   idx  [B][T][K] int32, any order, -1 = empty slot (duplicates count twice)
+ *   gate [B][T][64] bf16 or NULL     out [B][T][64][512] bf16 (output; 16-byte
+ *        aligned)
+ * The contractions accumulate in fp32; the softmax weights are rounded to fp16
+ * for the second one.  Within a head, query latent values below 2^-31 of the
+ * head's largest one lose low bits.  A query with no valid slot gets zeros.
+ * Rows that idx does not name are not read, whatever they hold.  Workspace:
+ * 256 bytes.  Device error: an index outside [-1, L) (the slot is treated as
+ * empty). */
+SGA_API sga_status_t sga_sparse_mla_attend_kv4(const sga_dims_t* dims, const sga_bf16_t* q, const uint8_t* kv4,
+                                               const int32_t* idx, const sga_bf16_t* gate, sga_bf16_t* out, void* ws,
+                                               size_t ws_bytes, sga_stream_t stream);
+
+/* sga_forward with the 4-bit latent cache: sga_index_scores ->
+ * sga_topk_select -> sga_sparse_mla_attend_kv4 (the indexer reads its own bf16
+ * key cache, so the indices are those of sga_forward).  The workspace is
+ * sga_workspace_size(dims, SGA_OP_FORWARD) bytes, zero-filled before the first
+ * call, as for sga_forward; idx_out may be NULL. */
+SGA_API sga_status_t sga_forward_kv4(const sga_dims_t* dims, const sga_bf16_t* q_idx, const sga_bf16_t* w,
+                                     const sga_bf16_t* k_idx, const sga_bf16_t* q, const uint8_t* kv4,
+                                     const sga_bf16_t* gate, const int32_t* q_pos, int32_t* idx_out,
+                                     sga_bf16_t* out, void* ws, size_t ws_bytes, sga_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Products with weights in E4M3 and a scale for each block of 128 (nlp.com.ai
+ * "A.X K2 FP8": 128 x 128 weight blocks, dynamic activation scaling). */
+
+/* Activations to E4M3, one scale for each token and block of 128 channels:
+ *   scale[t][j] = 2^e, the smallest e >= -126 with max|x| <= 448 * 2^e over the
+ *                 block (1 for a block of zeros)
+ *   codes[t][c] = the E4M3 value nearest to x[t][c] / scale (ties to even)
+ * The scale is a power of two, so the division is exact.  An infinity counts
+ * as the largest bf16 and becomes +-448; a NaN stays a NaN and does not count.
+ *   x [rows][cols] bf16    codes [rows][cols] E4M3 bytes
+ *   scale [rows][ceil(cols / 128)] fp32
+ * cols is a multiple of 16; x and codes 16-byte aligned. */
+SGA_API sga_status_t sga_quantize_fp8(int32_t rows, int32_t cols, const sga_bf16_t* x, sga_fp8_e4m3_t* codes,
+                                      float* scale, sga_stream_t stream);
+
+typedef enum { SGA_OUT_FP32 = 0, SGA_OUT_BF16 = 1 } sga_out_type_t;
+
+/* Bytes of workspace sga_gemm_fp8 needs, whatever the sizes: a status word,
+ * counters and the fp32 partial sums of output tiles that several thread blocks
+ * share.  Zero-filled before the first call; every call leaves the counters
+ * zeroed for the next one (after a device error, zero it again). */
+#define SGA_GEMM_FP8_WORKSPACE_BYTES (24 * 1024 * 1024)
+
+/* The block-scaled product y = x w^T of n tokens and m output channels:
+ *   y[t][i] = sum_j x_scale[t][j] w_scale[i / 128][j]
+ *             sum_{c in block j of 128} x[t][c] w[i][c]
+ *   x [n][k] E4M3 bytes    x_scale [n][ceil(k / 128)] fp32
+ *   w [m][k] E4M3 bytes    w_scale [ceil(m / 128)][ceil(k / 128)] fp32
+ *   y [n][m] fp32 or bf16 (out_type)
+ * The scales are any fp32 values.  A block's products accumulate in fp32 in
+ * the tensor core, the scaled blocks in fp32 in a fixed order (results do not
+ * depend on the schedule); a bf16 y is rounded once.  k is a multiple of 16; x
+ * and w 16-byte aligned, y aligned to its elements.  The last blocks may be
+ * partial. */
+SGA_API sga_status_t sga_gemm_fp8(int32_t n, int32_t m, int32_t k, const sga_fp8_e4m3_t* x, const float* x_scale,
+                                  const sga_fp8_e4m3_t* w, const float* w_scale, void* y, sga_out_type_t out_type,
+                                  void* ws, size_t ws_bytes, sga_stream_t stream);
+
 /* Synchronises `stream` and returns in *device_status the first device-side
  * error recorded in the workspace (an sga_status_t value, SGA_OK if none). */
 SGA_API sga_status_t sga_get_device_status(const void* ws, sga_stream_t stream, int32_t* device_status);

@@ -39,8 +39,15 @@ EXPORTED = ["sga_abi_version", "sga_status_string", "sga_workspace_size", "sga_i
             "sga_sparse_mla_attend", "sga_forward", "sga_get_device_status", "sga_clear_device_status",
             "sga_topk_select_noalloc", "sga_index_scores_fp8", "sga_forward_fp8", "sga_layer_workspace_size",
             "sga_layer_project", "sga_layer_output", "sga_layer_forward", "sga_indexer_warmup_workspace_size",
-            "sga_indexer_warmup", "sga_selftest_bounded_wait", "sga_forward_fused", "sga_forward_fused_fp8"]
+            "sga_indexer_warmup", "sga_selftest_bounded_wait", "sga_forward_fused", "sga_forward_fused_fp8",
+            "sga_kv4_append", "sga_kv4_read", "sga_sparse_mla_attend_kv4", "sga_forward_kv4", "sga_quantize_fp8",
+            "sga_gemm_fp8"]
 NOALLOC_SCRATCH_BYTES = 256 + 4 * 1024 * 1024
+KV4_ROW_BYTES = 416  # one row of the 4-bit latent cache (see sga_kv4_append)
+FP8_BLOCK = 128  # channels (and weight rows) that share a scale
+GEMM_FP8_WORKSPACE_BYTES = 24 * 1024 * 1024
+STATUS_BYTES = 256  # the workspace of a call that keeps only its status word there
+OUT_FP32, OUT_BF16 = 0, 1
 
 
 class SGAError(RuntimeError):
@@ -98,6 +105,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "sga_layer_forward": (ctypes.c_int, [D, ctypes.POINTER(LayerWeights), P, P, P, P, P, P, P, sz, P]),
         "sga_indexer_warmup_workspace_size": (ctypes.c_int, [D, ctypes.POINTER(sz)]),
         "sga_indexer_warmup": (ctypes.c_int, [D, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "sga_kv4_append": (ctypes.c_int, [D, P, P, P, P, sz, P]),
+        "sga_kv4_read": (ctypes.c_int, [D, P, P, P, P, sz, P]),
+        "sga_sparse_mla_attend_kv4": (ctypes.c_int, [D, P, P, P, P, P, P, sz, P]),
+        "sga_forward_kv4": (ctypes.c_int, [D, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "sga_quantize_fp8": (ctypes.c_int, [i32, i32, P, P, P, P]),
+        "sga_gemm_fp8": (ctypes.c_int, [i32, i32, i32, P, P, P, P, P, ctypes.c_int, P, sz, P]),
         "sga_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int64, P, sz, P]),
     }
     for name, (res, args) in sig.items():
@@ -135,6 +148,14 @@ def _need(t, name, dtype, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
+
+
+def _one_device(*tensors):
+    """Every given tensor lives on the current CUDA device: the library launches there, on its streams."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"expected every tensor on the current device {dev}, got one on {t.device}")
 
 
 def _need_fp8(t, name, shape):
@@ -322,6 +343,152 @@ def forward_fused_fp8(q_idx, w, k_idx, q, kv, gate, q_pos, top_k: int = TOP_K, i
     """`forward_fused` with E4M3 indexer queries and keys: the results of `forward_fp8`."""
     return _forward_call("sga_forward_fused_fp8", True, OP_FORWARD_FUSED, q_idx, w, k_idx, q, kv, gate, q_pos,
                          top_k, idx_out, out, ws, stream, return_idx)
+
+
+# ----------------------------------------------------------------------------- the latent cache in 4 bits
+def _status_ws(ws, device):
+    return torch.zeros(STATUS_BYTES, dtype=torch.uint8, device=device) if ws is None else ws
+
+
+def kv4_append(kv_rows, q_pos, kv4, ws=None, stream=None):
+    """Quantises kv_rows [B,T,576] bf16 into the 4-bit cache kv4 [B,L,416] uint8 at q_pos [B,T]
+    (sga_kv4_append); returns kv4, written in place."""
+    B, T = kv_rows.shape[0], kv_rows.shape[1]
+    L = kv4.shape[1]
+    _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
+    _need(q_pos, "q_pos", torch.int32, (B, T))
+    _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
+    dims = make_dims(B, T, L)
+    ws = _status_ws(ws, kv4.device)
+    _one_device(kv_rows, q_pos, kv4, ws)
+    _check("sga_kv4_append", load_library().sga_kv4_append(
+        ctypes.byref(dims), _ptr(kv_rows), _ptr(q_pos), _ptr(kv4), _ptr(ws), ws.numel(), _stream(stream)))
+    return kv4
+
+
+def kv4_read(kv4, pos, kv_rows=None, ws=None, stream=None):
+    """The values [B,T,576] bf16 of the 4-bit cache's rows at pos [B,T] (sga_kv4_read); zeros where pos is -1."""
+    B, T = pos.shape
+    L = kv4.shape[1]
+    _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
+    _need(pos, "pos", torch.int32, (B, T))
+    if kv_rows is None:
+        kv_rows = torch.empty((B, T, QK_DIM), dtype=torch.bfloat16, device=kv4.device)
+    _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
+    dims = make_dims(B, T, L)
+    ws = _status_ws(ws, kv4.device)
+    _one_device(kv4, pos, kv_rows, ws)
+    _check("sga_kv4_read", load_library().sga_kv4_read(
+        ctypes.byref(dims), _ptr(kv4), _ptr(pos), _ptr(kv_rows), _ptr(ws), ws.numel(), _stream(stream)))
+    return kv_rows
+
+
+def sparse_mla_attend_kv4(q, kv4, idx, gate=None, out=None, ws=None, stream=None):
+    """Sparse latent attention over the 4-bit cache + sigmoid head gate -> out [B,T,64,512] bf16."""
+    B, T = q.shape[0], q.shape[1]
+    L = kv4.shape[1]
+    K = idx.shape[-1]
+    _need(q, "q", torch.bfloat16, (B, T, HEADS, QK_DIM))
+    _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
+    _need(idx, "idx", torch.int32, (B, T, K))
+    if gate is not None:
+        _need(gate, "gate", torch.bfloat16, (B, T, HEADS))
+    dims = make_dims(B, T, L, K)
+    if out is None:
+        out = torch.empty((B, T, HEADS, V_DIM), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
+    ws = _status_ws(ws, q.device)
+    _one_device(q, kv4, idx, gate, out, ws)
+    _check("sga_sparse_mla_attend_kv4", load_library().sga_sparse_mla_attend_kv4(
+        ctypes.byref(dims), _ptr(q), _ptr(kv4), _ptr(idx), _ptr(gate), _ptr(out), _ptr(ws), ws.numel(),
+        _stream(stream)))
+    return out
+
+
+def forward_kv4(q_idx, w, k_idx, q, kv4, gate, q_pos, top_k: int = TOP_K, idx_out=None, out=None, ws=None,
+                stream=None, return_idx: bool = True):
+    """The whole path over the 4-bit latent cache (sga_forward_kv4).  Returns (idx [B,T,K] or None,
+    out [B,T,64,512] bf16)."""
+    B, T = q_idx.shape[0], q_idx.shape[1]
+    L = k_idx.shape[1]
+    _need(q_idx, "q_idx", torch.bfloat16, (B, T, INDEX_HEADS, INDEX_DIM))
+    _need(w, "w", torch.bfloat16, (B, T, INDEX_HEADS))
+    _need(k_idx, "k_idx", torch.bfloat16, (B, L, INDEX_DIM))
+    _need(q, "q", torch.bfloat16, (B, T, HEADS, QK_DIM))
+    _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
+    if gate is not None:
+        _need(gate, "gate", torch.bfloat16, (B, T, HEADS))
+    _need(q_pos, "q_pos", torch.int32, (B, T))
+    dims = make_dims(B, T, L, top_k)
+    if idx_out is None and return_idx:
+        idx_out = torch.empty((B, T, top_k), dtype=torch.int32, device=q.device)
+    if idx_out is not None:
+        _need(idx_out, "idx_out", torch.int32, (B, T, top_k))
+    if out is None:
+        out = torch.empty((B, T, HEADS, V_DIM), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
+    if ws is None:
+        ws = alloc_workspace(dims, OP_FORWARD, q.device)
+    _one_device(q_idx, w, k_idx, q, kv4, gate, q_pos, idx_out, out, ws)
+    _check("sga_forward_kv4", load_library().sga_forward_kv4(
+        ctypes.byref(dims), _ptr(q_idx), _ptr(w), _ptr(k_idx), _ptr(q), _ptr(kv4), _ptr(gate), _ptr(q_pos),
+        _ptr(idx_out), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    return idx_out, out
+
+
+# ----------------------------------------------------------------------------- products in E4M3, a scale per block of 128
+def quantize_fp8(x, codes=None, scale=None, stream=None):
+    """bf16 activations x [..., K] -> (codes [..., K] float8_e4m3fn, scale [..., ceil(K / 128)] fp32): one
+    power-of-two scale for each token and block of 128 channels (sga_quantize_fp8)."""
+    _need(x, "x", torch.bfloat16)
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError("x: must have at least one element")
+    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    _need_fp8(codes, "codes", x.shape)
+    if scale is None:
+        scale = torch.empty((*lead, -(-K // FP8_BLOCK)), dtype=torch.float32, device=x.device)
+    _need(scale, "scale", torch.float32, (*lead, -(-K // FP8_BLOCK)))
+    _one_device(x, codes, scale)
+    _check("sga_quantize_fp8", load_library().sga_quantize_fp8(
+        x.numel() // K, K, _ptr(x), _ptr(codes), _ptr(scale), _stream(stream)))
+    return codes, scale
+
+
+def alloc_gemm_fp8_workspace(device=None) -> torch.Tensor:
+    """A zero-filled workspace for gemm_fp8, of any sizes."""
+    return torch.zeros(GEMM_FP8_WORKSPACE_BYTES, dtype=torch.uint8, device=device or "cuda")
+
+
+def gemm_fp8(x, x_scale, w, w_scale, out_dtype=torch.float32, out=None, ws=None, stream=None):
+    """The product x w^T of E4M3 activations x [..., K] and weights w [M, K] with the scales x_scale
+    [..., ceil(K / 128)] and w_scale [ceil(M / 128), ceil(K / 128)] fp32 (sga_gemm_fp8) -> [..., M], fp32 or bf16."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x: expected [..., K] and w: [M, K]")
+    M, K = w.shape
+    lead = tuple(x.shape[:-1])
+    kb = -(-K // FP8_BLOCK)
+    x = _need_fp8(x, "x", (*lead, K))
+    w = _need_fp8(w, "w", (M, K))
+    _need(x_scale, "x_scale", torch.float32, (*lead, kb))
+    _need(w_scale, "w_scale", torch.float32, (-(-M // FP8_BLOCK), kb))
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
+    if x.numel() == 0 or M == 0:
+        raise ValueError("x, w: must have at least one element")
+    if out is None:
+        out = torch.empty((*lead, M), dtype=out_dtype, device=x.device)
+    _need(out, "out", out_dtype, (*lead, M))
+    if ws is None:
+        ws = alloc_gemm_fp8_workspace(x.device)
+    _one_device(x, x_scale, w, w_scale, out, ws)
+    _check("sga_gemm_fp8", load_library().sga_gemm_fp8(
+        x.numel() // K, M, K, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(out),
+        OUT_BF16 if out_dtype == torch.bfloat16 else OUT_FP32, _ptr(ws), ws.numel(), _stream(stream)))
+    return out
 
 
 # ----------------------------------------------------------------------------- one SGA layer

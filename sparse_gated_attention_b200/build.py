@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsga.so")
 LIB_DEBUG = os.path.join(PKG, "libsga_debug.so")  # SGA_DEBUG: device invariant checks
 SOURCES = ["sga_api.cu", "sga_index.cu", "sga_topk.cu", "sga_attend.cu", "sga_gemm.cu", "sga_layer.cu",
-           "sga_warmup.cu", "sga_diag.cu"]
+           "sga_warmup.cu", "sga_diag.cu", "sga_attend4.cu", "sga_kv4.cu", "sga_fp8.cu"]
 DEPS = SOURCES + ["sga_ptx.cuh", "sga_internal.cuh", "sga_host.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -17,6 +17,8 @@ namespace {
 using host::align_up;
 using host::aligned;
 using host::at;
+using host::device_info;
+using host::from_cuda;
 using host::kStatusBytes;
 constexpr size_t kAlign = host::kWsAlign;
 
@@ -74,38 +76,11 @@ Layout make_layout(const sga_dims_t& d, sga_op_t op) {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-// Checks that the current device is an sm_100 part and returns its SM count.
-sga_status_t device_info(int* num_sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return SGA_ERR_UNSUPPORTED;
-  }
-  int major = 0, sms = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return SGA_ERR_UNSUPPORTED;
-  }
-  if (major != 10) return SGA_ERR_UNSUPPORTED;
-  *num_sms = sms;
-  return SGA_OK;
-}
-
 sga_status_t check_ws(void* ws, size_t ws_bytes, const sga_dims_t& d, sga_op_t op, Layout* l) {
   *l = make_layout(d, op);
   if (!ws || !aligned(ws, kAlign)) return SGA_ERR_WORKSPACE;
   if (ws_bytes < l->total) return SGA_ERR_WORKSPACE;
   return SGA_OK;
-}
-
-// A failed launch or runtime call also leaves the error as the thread's last
-// CUDA error; it is cleared here so that it does not surface in the caller's
-// next, unrelated error check.
-sga_status_t from_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return SGA_OK;
-  cudaGetLastError();
-  return SGA_ERR_CUDA;
 }
 
 }  // namespace
@@ -164,11 +139,13 @@ sga_status_t index_scores_impl(const sga_dims_t* dims, const void* q_idx, const 
 sga_status_t forward_impl(const sga_dims_t* dims, const void* q_idx, const sga_bf16_t* w, const void* k_idx,
                           const sga_bf16_t* q, const sga_bf16_t* kv, const sga_bf16_t* gate, const int32_t* q_pos,
                           int32_t* idx_out, float* out, void* ws, size_t ws_bytes, sga_stream_t stream, bool fp8,
-                          bool fused, uint16_t* out_bf16 = nullptr) {
+                          bool fused, uint16_t* out_bf16 = nullptr, const uint8_t* kv4 = nullptr) {
   if (!dims_ok(dims)) return SGA_ERR_INVALID_ARG;
-  if (!aligned(q_idx, 16) || !aligned(w, 16) || !aligned(k_idx, 16) || !aligned(q, 16) || !aligned(kv, 16) ||
-      !aligned(q_pos, 4) || !aligned(out, 16) || (gate && !aligned(gate, 2)) || (idx_out && !aligned(idx_out, 16)) ||
-      (out_bf16 && !aligned(out_bf16, 8)))
+  // with the 4-bit cache, kv4 and out_bf16 stand in the place of kv and out
+  if (!aligned(q_idx, 16) || !aligned(w, 16) || !aligned(k_idx, 16) || !aligned(q, 16) ||
+      !aligned(kv4 ? static_cast<const void*>(kv4) : kv, 16) || !aligned(q_pos, 4) ||
+      !aligned(kv4 ? static_cast<void*>(out_bf16) : out, 16) || (gate && !aligned(gate, 2)) ||
+      (idx_out && !aligned(idx_out, 16)) || (out_bf16 && !aligned(out_bf16, 8)))
     return SGA_ERR_INVALID_ARG;
   Layout l;
   sga_status_t st = check_ws(ws, ws_bytes, *dims, fused ? SGA_OP_FORWARD_FUSED : SGA_OP_FORWARD, &l);
@@ -214,6 +191,11 @@ sga_status_t forward_impl(const sga_dims_t* dims, const void* q_idx, const sga_b
     }
   }
   if (e != cudaSuccess) return from_cuda(e);
+  if (kv4) {
+    host::NvtxRange range("sga.sparse_mla_attend_kv4");
+    Attend4Args aa{q, kv4, idx, gate, out_bf16, status, dims->batch, dims->n_q, dims->kv_stride, dims->top_k};
+    return from_cuda(launch_attend4(aa, s));
+  }
   host::NvtxRange range("sga.sparse_mla_attend");
   AttendArgs aa{q, kv, idx, gate, out, status, dims->batch, dims->n_q, dims->kv_stride, dims->top_k};
   aa.out_bf16 = out_bf16;
@@ -329,6 +311,15 @@ sga_status_t sga_forward_fused_fp8(const sga_dims_t* dims, const sga_fp8_e4m3_t*
                                    const sga_bf16_t* gate, const int32_t* q_pos, int32_t* idx_out, float* out,
                                    void* ws, size_t ws_bytes, sga_stream_t stream) {
   return forward_impl(dims, q_idx, w, k_idx, q, kv, gate, q_pos, idx_out, out, ws, ws_bytes, stream, true, true);
+}
+
+sga_status_t sga_forward_kv4(const sga_dims_t* dims, const sga_bf16_t* q_idx, const sga_bf16_t* w,
+                             const sga_bf16_t* k_idx, const sga_bf16_t* q, const uint8_t* kv4,
+                             const sga_bf16_t* gate, const int32_t* q_pos, int32_t* idx_out, sga_bf16_t* out,
+                             void* ws, size_t ws_bytes, sga_stream_t stream) {
+  if (!kv4) return SGA_ERR_INVALID_ARG;
+  return forward_impl(dims, q_idx, w, k_idx, q, nullptr, gate, q_pos, idx_out, nullptr, ws, ws_bytes, stream, false,
+                      false, out, kv4);
 }
 
 sga_status_t sga_get_device_status(const void* ws, sga_stream_t stream, int32_t* device_status) {

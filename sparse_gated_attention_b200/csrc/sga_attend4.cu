@@ -1,0 +1,745 @@
+// Sparse MLA attention over a latent cache held in 4 bits, then the head-specific
+// sigmoid gate: the formulas of sga_attend.cu on rows of 416 bytes (512 E2M1
+// codes, an E4M3 scale for each 16 of them, 64 bf16 rope values; see
+// sga_sparse_mla_attend_kv4 in sga.h).
+//
+//   S = Q C^T * 192^-0.5,  P = softmax_s(S),  out = (P C[:, 0:512]) * sigmoid(g)
+//
+// What differs from the bf16 kernel follows from the row being 2.8 times smaller:
+//   * A chunk's 64 rows are 26 KB, so they are gathered into registers: eight
+//     producer warps hold the next chunk's codes while they expand the current
+//     one, and the whole value ring in shared memory is left to expanded tiles.
+//   * A code times its scale has at most 6 significant bits between 2^-10 and
+//     2,688, so it is exact in fp16 (and in bf16).  The tiles hold fp16: two
+//     codes expand with one conversion and one multiplication, and P can be one
+//     fp16 operand (half a step is 2^-12, an eighth of the rounding of the bf16
+//     result) where the bf16 kernel needs two bf16 parts: half the PV
+//     instructions.
+//   * Q must then be fp16 for the latent dims.  Each head is scaled by the power
+//     of two that takes its largest value into [2^14, 2^15): a bf16 value keeps
+//     its 8 bits exactly down to 2^-31 of the head's largest, and the factor
+//     is taken out again in the softmax scale.  The rope dims stay bf16 on both
+//     sides (kind::f16 takes either type, one per instruction).
+// Everything else is as there: one CTA per (query, split), the splits of a query
+// a cluster; QK^T with M = 64 heads, N = 64 rows; PV transposed, O^T [512 x 64] in
+// tensor memory; a lazy running maximum in the log2 domain; the splits merged
+// through distributed shared memory.
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "sga_internal.cuh"
+#include "sga_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace sga {
+namespace {
+
+constexpr int kHeads = 64;
+constexpr int kDq = 576;
+constexpr int kDv = 512;
+constexpr int kChunk = 64;                   // selected rows per chunk
+constexpr int kBoxBytes = kChunk * 128;      // 64 rows x 64 dims of 16 bits
+constexpr int kPairBytes = 2 * kBoxBytes;    // 64 rows x 128 dims
+constexpr int kPairsPerChunk = 4;            // value dims 0..511
+constexpr int kPairRing = 8;                 // two chunks of value pairs
+constexpr int kRopeRing = 2;
+constexpr int kQBox = kHeads * 128;          // 64 heads x 64 dims
+constexpr int kQBytes = 9 * kQBox;
+constexpr int kQPieces = kDq / 8;            // 16-byte pieces of a query head
+constexpr int kPBytes = kHeads * kChunk * 2;  // 64 heads x 64 rows fp16
+constexpr int kMaskRing = 4;
+constexpr int kProducerWarps = 8;            // warps 0-7: four threads per chunk row
+constexpr int kMmaWarp = 8;
+constexpr int kSoftmaxThreads = 128;         // warps 9-12
+constexpr int kPvThread = (kMmaWarp + 1) * 32;  // the softmax thread that issues PV
+constexpr int kThreads = 32 * (kMmaWarp + 1) + kSoftmaxThreads;
+constexpr int kTmemCols = 512;
+constexpr int kSCol = 256;
+// barriers: pair_full[8] pair_empty[8] rope_full[2] rope_empty[2] q_full s_full[2] s_free[2]
+//           qk_done p_free o_full mask_full[4] mask_empty[4]
+constexpr int kNumBars = 2 * kPairRing + 2 * kRopeRing + 1 + 2 + 2 + 3 + 2 * kMaskRing;
+constexpr int kMaxSplits = 8;                // splits of a query = CTAs of its cluster
+constexpr size_t kSmemBytes = 1024 + kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes + kPBytes +
+                              kNumBars * 8 + kMaskRing * 8 + 2 * kHeads * 4 + kHeads * 8 + 16;
+constexpr float kRescaleThreshold = 8.0f;    // log2 units
+// P = 2^(x - max + 7): with a maximum that lags by at most 8 it stays within 2^15 and inside fp16, and fp16's
+// smallest step is 2^-31 of the largest weight (the factor 2^7 is in O and in l alike and cancels).
+constexpr float kPShift = 7.0f;
+constexpr int kRowBytes = SGA_KV4_ROW_BYTES;
+constexpr int kScaleOff = kDv / 2;           // byte offset of a row's scales
+constexpr int kRopeOff = kScaleOff + kDv / 16;
+
+static_assert(kRowBytes == kRopeOff + 2 * (kDq - kDv), "cache row layout");
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+// the split merge's receive buffer lies over the value ring, the rope slots and the Q buffer (see sga_attend.cu)
+static_assert(kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes >= 7 * kHeads * 76 * 4,
+              "split merge receive buffer");
+
+struct Attend4Params {
+  const uint16_t* q;
+  const uint8_t* kv4;
+  const int32_t* idx;
+  const uint16_t* gate;
+  uint16_t* out;
+  int* status;
+  int n_q, kv_stride, top_k, splits, chunks;
+  float scale_log2;
+};
+
+__device__ __forceinline__ float sigmoidf_(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+// 2^x with the hardware approximation (relative error ~2^-22; results below
+// 2^-126 flush to zero, which only drops weights far below the fp32 sum).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 16 bytes of the cache, read once per query: volatile keeps the load where it is issued, ahead of its use.
+__device__ __forceinline__ uint4 ld_row16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_row8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two E4M3 scales (the low 16 bits) -> each of them in both halves of an fp16 pair.
+__device__ __forceinline__ void expand_scales(uint32_t two, uint32_t& s0, uint32_t& s1) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
+  s0 = __byte_perm(h, h, 0x1010);
+  s1 = __byte_perm(h, h, 0x3232);
+}
+
+// Eight E2M1 codes (code 2j in the low half of byte j) times one scale -> eight fp16 values (exact).
+__device__ __forceinline__ uint4 expand_codes(uint32_t codes, uint32_t scale) {
+  uint4 v;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "r"(codes));
+  v.x = hmul2(v.x, scale);
+  v.y = hmul2(v.y, scale);
+  v.z = hmul2(v.z, scale);
+  v.w = hmul2(v.w, scale);
+  return v;
+}
+
+// The part of one cache row that one of its four producer threads (part = 0..3) expands: 32 codes of every
+// 128-dim pair, the scales of pair `part` (exchanged among the four threads) and 16 rope values.
+struct RowPart {
+  uint4 codes[kPairsPerChunk];
+  uint2 scales;
+  uint4 rope[2];
+};
+
+__device__ __forceinline__ void load_row(RowPart& d, const uint8_t* row, int part, bool valid) {
+  if (valid) {
+#pragma unroll
+    for (int q = 0; q < kPairsPerChunk; ++q) d.codes[q] = ld_row16(row + 64 * q + 16 * part);
+    d.scales = ld_row8(row + kScaleOff + 8 * part);
+    d.rope[0] = ld_row16(row + kRopeOff + 32 * part);
+    d.rope[1] = ld_row16(row + kRopeOff + 32 * part + 16);
+  } else {  // an empty slot: zeros (masked out of the softmax)
+#pragma unroll
+    for (int q = 0; q < kPairsPerChunk; ++q) d.codes[q] = make_uint4(0, 0, 0, 0);
+    d.scales = make_uint2(0, 0);
+    d.rope[0] = d.rope[1] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t pairs = smem_u32(smem);
+  const uint32_t rope = pairs + kPairRing * kPairBytes;
+  const uint32_t q_s = rope + kRopeRing * kBoxBytes;
+  const uint32_t p_s = q_s + kQBytes;
+  uint8_t* p_ptr = smem + kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(p_ptr + kPBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto pair_full = [&](int s) { return bar0 + 8u * s; };
+  auto pair_empty = [&](int s) { return bar0 + 8u * (kPairRing + s); };
+  auto rope_full = [&](int s) { return bar0 + 8u * (2 * kPairRing + s); };
+  auto rope_empty = [&](int s) { return bar0 + 8u * (2 * kPairRing + kRopeRing + s); };
+  const uint32_t q_full = bar0 + 8u * (2 * kPairRing + 2 * kRopeRing);
+  auto s_full = [&](int b) { return q_full + 8u * (1 + b); };
+  auto s_free = [&](int b) { return q_full + 8u * (3 + b); };
+  const uint32_t qk_done = q_full + 8u * 5;  // every QK^T MMA of the MMA warp has finished
+  const uint32_t p_free = q_full + 8u * 6;
+  const uint32_t o_full = q_full + 8u * 7;
+  auto mask_full = [&](int b) { return q_full + 8u * (8 + b); };
+  auto mask_empty = [&](int b) { return q_full + 8u * (8 + kMaskRing + b); };
+  uint64_t* masks = bars + kNumBars;
+  float* head_f = reinterpret_cast<float*>(masks + kMaskRing);  // [64] per-head factors
+  float* q_scale = head_f + kHeads;                              // [64] softmax scale (log2) of the scaled heads
+  float2* own_ml = reinterpret_cast<float2*>(q_scale + kHeads);  // [64] (m, l) of this split, read by the cluster
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(own_ml + kHeads);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int row = blockIdx.x / p.splits;
+  const int split = static_cast<int>(cluster.block_rank());  // the cluster is the query's p.splits CTAs
+  const int chunk0 = p.chunks * split / p.splits;            // at most 32 chunks, at least one per split
+  const int nchunks = p.chunks * (split + 1) / p.splits - chunk0;
+  const int slot_base = chunk0 * kChunk;                     // first selected slot of this split
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairRing; ++s) {
+      mbar_init(pair_full(s), kProducerWarps);
+      mbar_init(pair_empty(s), 1);
+    }
+    for (int s = 0; s < kRopeRing; ++s) {
+      mbar_init(rope_full(s), kProducerWarps);
+      mbar_init(rope_empty(s), 1);
+    }
+    mbar_init(q_full, kProducerWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full(b), 1);
+      mbar_init(s_free(b), kSoftmaxThreads);
+    }
+    mbar_init(qk_done, 1);
+    mbar_init(p_free, 1);
+    mbar_init(o_full, 1);
+    for (int b = 0; b < kMaskRing; ++b) {
+      mbar_init(mask_full(b), kProducerWarps);
+      mbar_init(mask_empty(b), kSoftmaxThreads);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Set-up above overlaps the previous kernel on the stream; every input is read below.
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp < kProducerWarps) {
+    // ------------------------------------------------------------ gather and expansion
+    const int b = row / p.n_q;
+    const int32_t* idx_row = p.idx + static_cast<size_t>(row) * p.top_k;
+    const uint8_t* kv_b = p.kv4 + static_cast<size_t>(b) * p.kv_stride * kRowBytes;
+    const int ptid = threadIdx.x;
+    const int r = ptid >> 2;    // this thread's row of the chunk
+    const int part = ptid & 3;  // and its quarter of that row
+    bool ok = true;
+    auto load_idx = [&](int j) {
+      if (j >= nchunks) return -1;
+      const int v = __ldg(idx_row + slot_base + j * kChunk + r);  // K is a multiple of 64: a chunk has no tail
+      if (v < -1 || v >= p.kv_stride) {
+        record_status(p.status, kStatusDeviceArg);
+        return -1;
+      }
+      return v;
+    };
+    auto load = [&](RowPart& d, int v) {
+      load_row(d, kv_b + static_cast<size_t>(v < 0 ? 0 : v) * kRowBytes, part, v >= 0);
+    };
+    int cur_idx = load_idx(0), next_idx = load_idx(1);
+    RowPart next;
+    load(next, cur_idx);
+    {
+      // Q: four threads per head, 16-byte pieces part, part + 4, ...; pieces 64.. are the rope dims
+      const int h = r;
+      const uint8_t* q_row = reinterpret_cast<const uint8_t*>(p.q) + (static_cast<size_t>(row) * kHeads + h) * kDq * 2;
+      uint4 v[kQPieces / 4];
+#pragma unroll
+      for (int i = 0; i < kQPieces / 4; ++i) v[i] = ld_row16(q_row + 16 * (part + 4 * i));
+      uint32_t top = 0;  // largest magnitude as bf16 bits
+#pragma unroll
+      for (int i = 0; i < kQPieces / 4; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+      }
+      top = max(top & 0xFFFFu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      // 2^e takes a largest value of exponent x to exponent 14; heads smaller than 2^-86 have logits of zero anyway
+      int e = 14 + 127 - static_cast<int>(top >> 7);
+      e = top == 0 ? 0 : min(max(e, -113), 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < kQPieces / 4; ++i) {
+        const int c = part + 4 * i;
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float lo = __uint_as_float(w[k] << 16) * up, hi = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+          o[k] = i < kDv / 32 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+        }
+        st_shared16(q_s + (c >> 3) * kQBox + h * 128 + (((c & 7) ^ (h & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      if (part == 0) q_scale[h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    for (int j = 0; j < nchunks; ++j) {
+      const RowPart cur = next;
+      const uint32_t seen = __ballot_sync(0xFFFFFFFFu, cur_idx >= 0);
+      if (j + 1 < nchunks) {
+        cur_idx = next_idx;
+        load(next, cur_idx);
+        next_idx = load_idx(j + 2);
+      }
+      {
+        // validity of the warp's eight rows (every fourth ballot bit) -> bits 8 warp .. of the chunk's mask
+        uint32_t m = seen & 0x11111111u;
+        m = (m | (m >> 3)) & 0x03030303u;
+        m = (m | (m >> 6)) & 0x000F000Fu;
+        m = (m | (m >> 12)) & 0xFFu;
+        if (lane == 0) {
+          const int mb = j % kMaskRing;
+          if (mbar_wait(mask_empty(mb), static_cast<uint32_t>((j / kMaskRing) & 1) ^ 1u, abort_flag)) {
+            reinterpret_cast<uint8_t*>(masks + mb)[warp] = static_cast<uint8_t>(m);
+            mbar_arrive(mask_full(mb));
+          } else {
+            ok = false;
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+      }
+      const int rs = j % kRopeRing;
+      ok = mbar_wait(rope_empty(rs), static_cast<uint32_t>((j / kRopeRing) & 1) ^ 1u, abort_flag);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        st_shared16(rope + rs * kBoxBytes + r * 128 + (((2 * part + i) ^ (r & 7)) << 4), cur.rope[i]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rope_full(rs));
+      // value dims 128 q .. 128 q + 127 -> pair slot (4 j + q) mod 8; this thread's 32 dims are four
+      // 16-byte columns of box part / 2.  The upper box's threads store their columns in the order
+      // 2, 3, 0, 1, so the eight threads of a store phase reach eight different columns.
+      const uint32_t flip = part & 2;
+      const uint32_t dst0 = (part >> 1) * kBoxBytes + r * 128;
+      const uint32_t col0 = (part & 1) * 4;
+#pragma unroll
+      for (int q = 0; q < kPairsPerChunk; ++q) {
+        const int n = j * kPairsPerChunk + q;
+        const int slot = n % kPairRing;
+        ok = mbar_wait(pair_empty(slot), static_cast<uint32_t>((n / kPairRing) & 1) ^ 1u, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        // the scales of pair q are with thread q of the row's four; this thread's two are its half word `part`
+        const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, cur.scales.x, (lane & ~3) + q);
+        const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, cur.scales.y, (lane & ~3) + q);
+        const uint32_t two = ((part & 2) ? w1 : w0) >> (16 * (part & 1));
+        uint32_t s0, s1;
+        expand_scales(two & 0xFFFFu, s0, s1);
+        const uint4 c = cur.codes[q];
+        const uint32_t a0 = flip ? c.z : c.x, a1 = flip ? c.w : c.y, a2 = flip ? c.x : c.z, a3 = flip ? c.y : c.w;
+        const uint32_t sa = flip ? s1 : s0, sb = flip ? s0 : s1;
+        const uint32_t base = pairs + slot * kPairBytes + dst0;
+        st_shared16(base + (((col0 + flip) ^ (r & 7)) << 4), expand_codes(a0, sa));
+        st_shared16(base + (((col0 + (1 ^ flip)) ^ (r & 7)) << 4), expand_codes(a1, sa));
+        st_shared16(base + (((col0 + (2 ^ flip)) ^ (r & 7)) << 4), expand_codes(a2, sb));
+        st_shared16(base + (((col0 + (3 ^ flip)) ^ (r & 7)) << 4), expand_codes(a3, sb));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pair_full(slot));
+      }
+      if (!ok) break;
+    }
+    if (!ok) {
+      record_status(p.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_lat = idesc_f16_f32(kHeads, kChunk, false, false);
+      constexpr uint32_t idesc_rope = idesc_bf16_f32(kHeads, kChunk, false, false);
+      bool ok = mbar_wait(q_full, 0, abort_flag);
+      // Non-blocking issue of QK^T(qk_j), piece by piece: part 0 is the rope
+      // box (once the S buffer and the rope slot are ready), parts 1-4 one
+      // value pair each.
+      int qk_j = 0, qk_part = 0;
+      long long idle_since = clock64();
+      while (ok && qk_j < nchunks) {
+        bool did = false;
+        const int sb = qk_j & 1;
+        const uint32_t d = tmem + kSCol + sb * kChunk;
+        if (qk_part == 0) {
+          const int rs = qk_j % kRopeRing;
+          if (mbar_test_wait(s_free(sb), static_cast<uint32_t>((qk_j >> 1) & 1) ^ 1u) &&
+              mbar_test_wait(rope_full(rs), static_cast<uint32_t>((qk_j / kRopeRing) & 1))) {
+            tc_fence_after();
+            const uint32_t src = rope + rs * kBoxBytes;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16(d, sdesc_sw128(q_s + 8 * kQBox + kk * 32, 16, 1024), sdesc_sw128(src + kk * 32, 16, 1024),
+                       idesc_rope, kk > 0 ? 1u : 0u);
+            mma_commit(rope_empty(rs));  // rope dims are not needed for P V
+            qk_part = 1;
+            did = true;
+          }
+        } else {
+          const int q = qk_part - 1;
+          const int n = qk_j * kPairsPerChunk + q;
+          const int slot = n % kPairRing;
+          if (mbar_test_wait(pair_full(slot), static_cast<uint32_t>((n / kPairRing) & 1))) {
+            tc_fence_after();
+            const uint32_t base = pairs + slot * kPairBytes;
+#pragma unroll
+            for (int bx = 0; bx < 2; ++bx) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16(d, sdesc_sw128(q_s + (2 * q + bx) * kQBox + kk * 32, 16, 1024),
+                         sdesc_sw128(base + bx * kBoxBytes + kk * 32, 16, 1024), idesc_lat, 1u);
+            }
+            if (qk_part == kPairsPerChunk) {
+              mma_commit(s_full(sb));
+              ++qk_j;
+              qk_part = 0;
+            } else {
+              ++qk_part;
+            }
+            did = true;
+          }
+        }
+        if (did) {
+          idle_since = clock64();
+        } else if (*abort_flag || clock64() - idle_since > kWaitBudgetCycles) {
+          ok = false;
+        }
+      }
+      if (!ok) {
+        record_status(p.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      mma_commit(qk_done);
+      volatile int never = 0;
+      mbar_wait(qk_done, 0, &never);  // every MMA this thread issued has finished
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    // As in sga_attend.cu: thread t of the warp holds rows t/4 and 8 + t/4 of its
+    // lane quarter, columns 8k + 2(t%4) and 8k + 2(t%4) + 1 for k = 0..7.
+    const int quarter = warp & 3;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const int m4 = lane & 3;
+    const int hrow[2] = {quarter * 16 + (lane >> 2), quarter * 16 + 8 + (lane >> 2)};  // this thread's two heads
+    float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    // Every softmax thread runs every iteration, even after a wait ran out
+    // (the abort flag then makes each later wait return at once), so the
+    // named barriers below always see all 128 threads.
+    bool ok = mbar_wait(q_full, 0, abort_flag);
+    const float sc[2] = {ok ? q_scale[hrow[0]] : 0.f, ok ? q_scale[hrow[1]] : 0.f};
+    for (int j = 0; j < nchunks; ++j) {
+      const int sb = j & 1;
+      ok = ok && mbar_wait(s_full(sb), static_cast<uint32_t>((j >> 1) & 1), abort_flag);
+      tc_fence_after();
+      float r[32];
+      tmem_ld_16x256b_x8(tmem + lane_addr + kSCol + sb * kChunk, r);
+      tc_fence_before();
+      mbar_arrive(s_free(sb));
+      const int mb = j % kMaskRing;
+      ok = ok && mbar_wait(mask_full(mb), static_cast<uint32_t>((j / kMaskRing) & 1), abort_flag);
+      const uint64_t mk = *reinterpret_cast<volatile uint64_t*>(masks + mb);
+      mbar_arrive(mask_empty(mb));
+      // x[i][2k + e] = score of row i at column 8k + 2 m4 + e (masked slots -> -inf)
+      float x[2][16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool valid = (mk >> (8 * k + 2 * m4 + e)) & 1ull;
+          x[0][2 * k + e] = valid ? r[4 * k + e] * sc[0] : -INFINITY;
+          x[1][2 * k + e] = valid ? r[4 * k + 2 + e] * sc[1] : -INFINITY;
+        }
+      }
+      float alpha[2];
+      bool resc = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mp[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mp[c] = fmaxf(fmaxf(x[i][4 * c], x[i][4 * c + 1]), fmaxf(x[i][4 * c + 2], x[i][4 * c + 3]));
+        float mt = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+        mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
+        mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2));
+        alpha[i] = 1.f;
+        if (m_ref[i] == -INFINITY) {
+          m_ref[i] = mt;  // nothing accumulated yet (all earlier weights were zero)
+        } else if (mt > m_ref[i] + kRescaleThreshold) {
+          alpha[i] = exp2f(m_ref[i] - mt);
+          m_ref[i] = mt;
+          resc = true;
+        }
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        if (m_ref[i] == -INFINITY) {  // every slot so far is empty: all weights are zero
+#pragma unroll
+          for (int c = 0; c < 16; ++c) x[i][c] = 0.f;
+        } else {
+          const float m_p = m_ref[i] - kPShift;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            x[i][c] = fast_exp2(x[i][c] - m_p);
+            ps[c & 3] += x[i][c];
+          }
+        }
+        float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        psum += __shfl_xor_sync(0xFFFFFFFFu, psum, 1);
+        psum += __shfl_xor_sync(0xFFFFFFFFu, psum, 2);
+        l_run[i] = l_run[i] * alpha[i] + psum;
+      }
+      // PV_{j-1} must be done before P and O are touched.
+      ok = ok && mbar_wait(p_free, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag);
+      tc_fence_after();
+      if (m4 == 0) {
+        head_f[hrow[0]] = alpha[0];
+        head_f[hrow[1]] = alpha[1];
+      }
+      if (named_barrier_or(1, kSoftmaxThreads, resc)) {
+        // O^T[dim][head] *= alpha[head]: every lane holds one dim of each block
+        for (int blk = 0; blk < 4; ++blk) {
+          for (int c = 0; c < 2; ++c) {
+            float o[32];
+            tmem_ld32(tmem + lane_addr + blk * kHeads + c * 32, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= head_f[c * 32 + i];
+            tmem_st32(tmem + lane_addr + blk * kHeads + c * 32, o);
+          }
+        }
+        named_barrier(1, kSoftmaxThreads);
+      }
+      // P[head][row] in the 128-byte-swizzled K-major layout (8 heads per 1 KB
+      // atom); this thread writes the fp16 pairs of columns 8k + 2 m4, +1.
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = hrow[i];
+        const uint32_t rbase = (h >> 3) * 1024 + (h & 7) * 128 + 4 * m4;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint32_t*>(p_ptr + rbase + ((k ^ (h & 7)) << 4)) = pack_f16(x[i][2 * k], x[i][2 * k + 1]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_barrier(2, kSoftmaxThreads);  // P_j (and any rescale of O) complete
+      if (threadIdx.x == kPvThread) {
+        // PV(j): O^T[dims 128 q ..][heads] += V_j^T P^T, one accumulator block per value pair
+        constexpr uint32_t idesc_pv = idesc_f16_f32(128, kHeads, true, false);
+        tc_fence_after();
+        for (int q = 0; q < kPairsPerChunk; ++q) {
+          const int slot = (j * kPairsPerChunk + q) % kPairRing;
+          const uint32_t base = pairs + slot * kPairBytes;
+          const uint32_t d = tmem + q * kHeads;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // A = V^T: M = 128 dims over the pair's two boxes, K = rows 16 kk ..
+            mma_bf16(d, sdesc_sw128(base + kk * 2048, kBoxBytes, 1024), sdesc_sw128(p_s + kk * 32, 16, 1024), idesc_pv,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(pair_empty(slot));
+        }
+        mma_commit(p_free);
+      }
+    }
+    if (threadIdx.x == kPvThread) mma_commit(o_full);  // every PV this thread issued
+    const bool have_o = ok && mbar_wait(o_full, 0, abort_flag);
+    if (!have_o) {
+      record_status(p.status, kStatusTimeout);
+      *abort_flag = 1;
+      if (threadIdx.x == kPvThread) {  // its MMAs must be done before TMEM is freed
+        volatile int never = 0;
+        mbar_wait(o_full, 0, &never);
+      }
+    }
+    if (m4 == 0) {
+      own_ml[hrow[0]] = make_float2(m_ref[0], l_run[0]);
+      own_ml[hrow[1]] = make_float2(m_ref[1], l_run[1]);
+    }
+  }
+
+  // ---- split merge, as in sga_attend.cu: out = g / L * sum_r 2^(m_r - M) O_r with
+  // M = max_r m_r and L = sum_r 2^(m_r - M) l_r (per head).  Every thread of the
+  // cluster takes part in its barriers, on every path.
+  const int S = p.splits;
+  float* o_stage = reinterpret_cast<float*>(smem);  // value ring + rope slots + Q buffer, idle after the MMAs
+  if (S > 1) {
+    cluster.sync();  // every split's (m, l) published; all MMAs of every CTA done
+  } else {
+    __syncthreads();
+  }
+  if (warp > kMmaWarp && lane < 16) {
+    const int head = (warp & 3) * 16 + lane;
+    const float g = p.gate ? sigmoidf_(bf16_bits_to_float(p.gate[static_cast<size_t>(row) * kHeads + head])) : 1.f;
+    float f;
+    if (S == 1) {
+      const float l = own_ml[head].y;
+      f = l == 0.f ? 0.f : g / l;
+    } else {
+      // every split's (m, l) for this head, all loads in flight at once
+      float2 ml[kMaxSplits];
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        ml[r] = r < S ? *cluster.map_shared_rank(&own_ml[head], r) : make_float2(-INFINITY, 0.f);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r) mx = fmaxf(mx, ml[r].x);
+      float L = 0.f;
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        if (ml[r].x != -INFINITY) L += exp2f(ml[r].x - mx) * ml[r].y;
+      const float m_own = own_ml[head].x;
+      f = (L != 0.f && m_own != -INFINITY) ? exp2f(m_own - mx) * g / L : 0.f;
+    }
+    head_f[head] = f;
+  }
+  __syncthreads();
+  // With several splits, CTA r owns the float4 columns [v0(r), v0(r+1)) of
+  // every head's 512 dims, v0(r) = 128 r / S; every CTA pushes its scaled O for
+  // those dims into the owner's receive buffer [source split][head][kStride].
+  const int kStride = 4 * ((kDv / 4 + S - 1) / S);  // floats per (source, head) row: the widest slice
+  float* recv = o_stage;
+  if (warp != kMmaWarp) {
+    // Twelve warps read O^T out of TMEM: warp w reads lane quarter w % 4; the
+    // producer warps 0-3 take dim block 0, 4-7 block 1, the softmax warps blocks 2-3.
+    // O^T block b: this lane holds dim 128 b + 32 quarter + lane for all 64 heads.
+    const int quarter = warp & 3;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const int blk0 = warp < 4 ? 0 : warp < kProducerWarps ? 1 : 2;
+    const int blk1 = warp < kProducerWarps ? blk0 + 1 : 4;
+    tc_fence_after();
+    for (int c = 0; c < 2; ++c) {
+      float hf[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) hf[i] = head_f[c * 32 + i];
+      for (int blk = blk0; blk < blk1; ++blk) {
+        const int dim = 128 * blk + 32 * quarter + lane;
+        float o[32];
+        tmem_ld32(tmem + lane_addr + blk * kHeads + c * 32, o);
+        if (S == 1) {
+          uint16_t* col = p.out + static_cast<size_t>(row) * kHeads * kDv + static_cast<size_t>(c * 32) * kDv + dim;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            col[static_cast<size_t>(i) * kDv] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * hf[i]));
+        } else {
+          const int v = dim >> 2;
+          const int owner = ((v + 1) * S - 1) / (kDv / 4);  // the r with v0(r) <= v < v0(r + 1)
+          const int dl = dim - 4 * ((kDv / 4) * owner / S);
+          float* col = cluster.map_shared_rank(recv + (split * kHeads + c * 32) * kStride + dl, owner);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) col[i * kStride] = o[i] * hf[i];
+        }
+      }
+    }
+  }
+  if (S > 1) {
+    cluster.sync();  // every split's scaled O delivered to its owners
+    const int v0 = (kDv / 4) * split / S, v1 = (kDv / 4) * (split + 1) / S;
+    const int vecs = v1 - v0;
+    uint16_t* orow = p.out + static_cast<size_t>(row) * kHeads * kDv;
+    for (int e = threadIdx.x; e < kHeads * vecs; e += kThreads) {
+      const int h = e / vecs, dv = e - h * vecs;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < S; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(recv + (r * kHeads + h) * kStride + 4 * dv);
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      *reinterpret_cast<uint2*>(orow + h * kDv + 4 * (v0 + dv)) =
+          make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Splits of the K slots per query (at most kMaxSplits, the CTAs of one cluster) so that rows * splits
+// fills ~148 SMs once; the chunks of 64 slots need not divide evenly.
+int attend4_splits(int rows, int chunks) {
+  int best = 1;
+  for (int s = 1; s <= chunks && s <= kMaxSplits; ++s)
+    if (static_cast<long long>(rows) * s <= 148) best = s;
+  return best;
+}
+
+}  // namespace
+
+cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t stream) {
+  const int rows = a.batch * a.n_q;
+  const cudaError_t e = cudaFuncSetAttribute(sga_attend4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmemBytes));
+  if (e != cudaSuccess) return e;
+  Attend4Params p;
+  p.q = a.q;
+  p.kv4 = a.kv4;
+  p.idx = a.idx;
+  p.gate = a.gate;
+  p.out = a.out;
+  p.status = a.status;
+  p.n_q = a.n_q;
+  p.kv_stride = a.kv_stride;
+  p.top_k = a.top_k;
+  p.chunks = a.top_k / kChunk;
+  p.splits = attend4_splits(rows, p.chunks);
+  p.scale_log2 = static_cast<float>(SGA_SOFTMAX_SCALE * 1.4426950408889634);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * p.splits));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sga_attend4_kernel, p);
+}
+
+}  // namespace sga

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/sga.h"
+
 namespace sga {
 namespace host {
 
@@ -22,6 +24,27 @@ inline bool aligned(const void* p, size_t a) { return p && (reinterpret_cast<uin
 template <class T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
+}
+
+// Checks that the current device is an sm_100 part and returns its SM count.
+inline sga_status_t device_info(int* num_sms) {
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SGA_ERR_UNSUPPORTED;
+  }
+  return major == 10 ? SGA_OK : SGA_ERR_UNSUPPORTED;
+}
+
+// A failed launch or runtime call also leaves the error as the thread's last
+// CUDA error; it is cleared here so that it does not surface in the caller's
+// next, unrelated error check.
+inline sga_status_t from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return SGA_OK;
+  cudaGetLastError();
+  return SGA_ERR_CUDA;
 }
 
 // One NVTX range (named after the stage it brackets) for the lifetime of the

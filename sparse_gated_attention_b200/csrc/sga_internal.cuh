@@ -90,6 +90,37 @@ struct AttendArgs {
 int attend_splits(int rows, int top_k);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream);
 
+// ---- attention over the 4-bit latent cache ------------------------------------------
+struct Attend4Args {
+  const uint16_t* q;     // [rows][64][576]
+  const uint8_t* kv4;    // [B][L][SGA_KV4_ROW_BYTES]
+  const int32_t* idx;    // [rows][K]
+  const uint16_t* gate;  // [rows][64] or null
+  uint16_t* out;         // [rows][64][512] bf16
+  int* status;
+  int batch, n_q, kv_stride, top_k;
+};
+cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t stream);
+
+// ---- the 4-bit cache's writer (arguments as sga_kv4_append's) -------------------------
+cudaError_t launch_kv4_append(const uint16_t* kv_rows, const int32_t* q_pos, uint8_t* kv4, int* status, int batch,
+                              int n_q, int kv_stride, cudaStream_t s);
+
+// ---- E4M3 products with a scale per block of 128 ----------------------------------------
+cudaError_t launch_quantize_fp8(int rows, int cols, const uint16_t* x, uint8_t* codes, float* scale, cudaStream_t s);
+struct GemmFp8Args {
+  int n, m, k;
+  const uint8_t* x;      // [n][k] E4M3
+  const float* x_scale;  // [n][ceil(k / 128)]
+  const uint8_t* w;      // [m][k] E4M3
+  const float* w_scale;  // [ceil(m / 128)][ceil(k / 128)]
+  float* out_f32;        // [n][m], or null
+  uint16_t* out_bf16;    // [n][m], or null
+  void* ws;              // SGA_GEMM_FP8_WORKSPACE_BYTES, counters zero
+  int* status;
+};
+cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int num_sms, cudaStream_t s);
+
 // ---- the layer's projections: weight-streaming GEMM -----------------------------------
 // Y[b][n][m] = sum_k X[n][x_col_per_batch * b + k] W[b](m, k), W row-major
 // [batch][m][k] (K-major) or [batch][k][m] (MN-major), bf16 in, fp32 accumulate.

@@ -62,6 +62,8 @@ constexpr double kRopeBase = 1.0e6;
 using sga::host::align_up;
 using sga::host::aligned;
 using sga::host::at;
+using sga::host::device_info;
+using sga::host::from_cuda;
 using sga::host::kStatusBytes;
 constexpr size_t kAlign = sga::host::kWsAlign;
 // The K splits (and so the workspace) are chosen for a 148-SM B200 whatever the
@@ -377,24 +379,6 @@ bool weights_ok(const sga_layer_weights_t* W, bool front, bool back) {
   return true;
 }
 
-// An sm_100 device: its SM count.
-sga_status_t device_sms(int* sms) {
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return SGA_ERR_UNSUPPORTED;
-  }
-  return major == 10 ? SGA_OK : SGA_ERR_UNSUPPORTED;
-}
-
-sga_status_t from_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return SGA_OK;
-  cudaGetLastError();
-  return SGA_ERR_CUDA;
-}
-
 // G1, P1, G2, P2, G3: the path's inputs for the new tokens.
 sga_status_t project_impl(const sga_dims_t& d, const sga_layer_weights_t* W, const uint16_t* h, const int32_t* q_pos,
                           uint16_t* kv_cache, uint16_t* kidx_cache, uint16_t* q, uint16_t* gate, uint16_t* q_idx,
@@ -503,7 +487,7 @@ sga_status_t sga_layer_project(const sga_dims_t* dims, const sga_layer_weights_t
   sga_status_t st = check_layer_ws(ws, ws_bytes, *dims, weights, SGA_LAYER_PROJECT, &l);
   if (st != SGA_OK) return st;
   int sms = 0;
-  if ((st = device_sms(&sms)) != SGA_OK) return st;
+  if ((st = device_info(&sms)) != SGA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return project_impl(*dims, weights, h, q_pos, kv_cache, k_idx_cache, q, gate, q_idx, w, ws, l, sms, s);
 }
@@ -516,7 +500,7 @@ sga_status_t sga_layer_output(const sga_dims_t* dims, const sga_layer_weights_t*
   sga_status_t st = check_layer_ws(ws, ws_bytes, *dims, weights, SGA_LAYER_OUTPUT, &l);
   if (st != SGA_OK) return st;
   int sms = 0;
-  if ((st = device_sms(&sms)) != SGA_OK) return st;
+  if ((st = device_info(&sms)) != SGA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return output_impl(*dims, weights, out, y, ws, l, sms, s);
 }
@@ -532,7 +516,7 @@ sga_status_t sga_layer_forward(const sga_dims_t* dims, const sga_layer_weights_t
   sga_status_t st = check_layer_ws(ws, ws_bytes, *dims, weights, SGA_LAYER_FORWARD, &l);
   if (st != SGA_OK) return st;
   int sms = 0;
-  if ((st = device_sms(&sms)) != SGA_OK) return st;
+  if ((st = device_info(&sms)) != SGA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint16_t* q = at<uint16_t>(ws, l.q);
   uint16_t* gate = at<uint16_t>(ws, l.gate);

@@ -1,0 +1,533 @@
+"""The low-bit operators on the GPU against their fp64 definitions (oracle/lowbit.py):
+activations in E4M3, products with a scale per block of 128, the 4-bit latent
+cache and the attention over it.
+
+Quantised values and the cache's bytes are compared exactly.  Tolerances of
+computed values follow the arithmetic:
+
+* product: a sum of k products and the scaled blocks, every addition rounded in
+  fp32 with at most one unit in the last place (2^-23): |error| <= (k + 2 kb + 2) 2^-23
+  sum |x w| scales, plus half a step (2^-8) of a bf16 result.  Where all values
+  are small integers the sums are exact and so is the comparison.
+* attention: half a step of the bf16 result, 2^-8 |out|; the softmax weights'
+  fp16 rounding and the fp32 sums, (2^-11 + 2^-14) sum p |v|; and the fp32 logits,
+  off by at most 41 additions * 2^-23 * sum |q k| scale each, which moves every
+  weight by twice that, relatively.  A weight P is held as 2^7 P in fp16, whose
+  subnormal step is 2^-24: below 2^-14 it is off by up to half of it, so P by
+  2^-32; the weights' sum is at least 1 in that scale, which adds at most
+  2^-32 sum |v| over the selected rows.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import lowbit
+import sparse_gated_attention_b200 as sga
+from sparse_gated_attention_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_gated_attention_b200 import build
+
+    build.build()
+    sga.load_library()
+    yield
+    torch.cuda.synchronize()
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV)
+
+
+def status_ws():
+    return torch.zeros(256, dtype=torch.uint8, device=DEV)
+
+
+def u8(x):
+    return x.view(torch.uint8).cpu().numpy()
+
+
+# ------------------------------------------------------------------------------------------------ quantiser
+def check_quantize(x):
+    codes, scale = sga.quantize_fp8(x)
+    want_codes, want_scale = lowbit.quantize_fp8(lowbit.to_f64(x.reshape(-1, x.shape[-1])))
+    got = u8(codes).reshape(want_codes.shape)
+    nan = (want_codes & 0x7F) == 0x7F
+    assert np.array_equal((got & 0x7F) == 0x7F, nan)
+    np.testing.assert_array_equal(got[~nan], want_codes[~nan])
+    np.testing.assert_array_equal(scale.cpu().numpy().reshape(want_scale.shape).astype(np.float64), want_scale)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 16), (3, 128), (5, 144), (1, 7168), (37, 272), (300, 1536)])
+def test_quantize_matches_definition(rows, cols):
+    g = gen(rows * 1000 + cols)
+    x = randn(g, rows, cols) * torch.exp2(torch.randint(-60, 60, (rows, 1), generator=g, device=DEV).float())
+    check_quantize(x.to(torch.bfloat16))
+
+
+def test_quantize_many_dims_and_rows_beyond_one_wave():
+    x = randn(gen(5), 3, 700, 272).to(torch.bfloat16)
+    check_quantize(x)
+
+
+def test_quantize_special_values():
+    """Zeros, one value alone, the border 448 * 2^e and the next value, rounding ties, the smallest and the
+    largest bf16 values, infinities and NaN."""
+    rows = []
+    base = np.zeros(128)
+
+    def add(*vals):
+        r = base.copy()
+        r[:len(vals)] = vals
+        rows.append(r)
+
+    add()
+    add(-0.0, 3.0)
+    add(448.0, 1.0)
+    add(450.0, 1.0, -225.0)  # above the border: scale 2
+    add(448.0, 17.0, 19.0, -17.0, 2.0 ** -10, 3 * 2.0 ** -10, 2.0 ** -9)  # ties of the normal and subnormal steps
+    add(2.0 ** -133, -(2.0 ** -133))  # subnormal bf16
+    add(2.0 ** -126, 2.0 ** -130)
+    add(3.3895313892515355e38, -1.0, 2.0 ** 100)
+    add(np.inf, 1.0, -np.inf, 3.3895313892515355e38)
+    add(np.nan, 5.0, -7.0)
+    x = torch.tensor(np.array(rows)).to(torch.bfloat16).to(DEV)
+    check_quantize(x)
+
+
+# ------------------------------------------------------------------------------------------------ product
+def rand_codes(g, *shape):
+    """Finite E4M3 bytes of every magnitude."""
+    c = torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.int32)
+    c = torch.where((c & 0x7F) == 0x7F, c - 1, c)
+    return c.to(torch.uint8)
+
+
+def product_case(n, m, k, seed):
+    g = gen(seed)
+    kb, mb = -(-k // 128), -(-m // 128)
+    xs = torch.exp2(torch.randint(-8, 8, (n, kb), generator=g, device=DEV).float()) * (1 + torch.rand((n, kb), generator=g, device=DEV))
+    ws = torch.rand((mb, kb), generator=g, device=DEV) * 0.01 + 1e-4
+    return rand_codes(g, n, k), xs, rand_codes(g, m, k), ws
+
+
+def check_product(n, m, k, out_dtype, seed=0, ws=None):
+    x, xs, w, wsc = product_case(n, m, k, seed)
+    ws = sga.alloc_gemm_fp8_workspace() if ws is None else ws
+    y = sga.gemm_fp8(x, xs, w, wsc, out_dtype=out_dtype, ws=ws)
+    assert y.dtype == out_dtype and tuple(y.shape) == (n, m)
+    assert sga.device_status(ws) == 0
+    X = torch.tensor(lowbit.block_scaled(x.cpu().numpy(), lowbit.to_f64(xs), 1), device=DEV)
+    W = torch.tensor(lowbit.block_scaled(w.cpu().numpy(), lowbit.to_f64(wsc), 128), device=DEV)
+    want, size = X @ W.T, X.abs() @ W.abs().T
+    tol = (k + 2 * xs.shape[1] + 2) * 2.0 ** -23 * size
+    if out_dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (want.abs() + tol)
+    err = (y.double() - want).abs()
+    assert bool((err <= tol).all()), f"max error / bound {(err / tol.clamp_min(1e-300)).max().item():.3f}"
+
+
+PRODUCT_SHAPES = [(1, 1, 16), (1, 128, 128), (2, 129, 144), (16, 64, 4112), (17, 300, 272), (31, 2304, 7168),
+                  (33, 1000, 1552), (64, 256, 512), (65, 130, 656), (127, 384, 1536), (129, 257, 400),
+                  (333, 1111, 1552), (512, 640, 2048), (1000, 300, 144)]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,m,k", PRODUCT_SHAPES)
+def test_product_matches_definition(n, m, k, out_dtype):
+    check_product(n, m, k, out_dtype, seed=n + m + k)
+
+
+@pytest.mark.parametrize("n,m,k", [(1, 7168, 8192), (4, 130, 20000), (40, 300, 1680), (300, 513, 1040)])
+def test_product_of_small_integers_is_exact(n, m, k):
+    """Codes of integers in [-2, 2] and power-of-two scales: every partial sum is exact."""
+    g = gen(n + k)
+    kb, mb = -(-k // 128), -(-m // 128)
+    x = torch.randint(-2, 3, (n, k), generator=g, device=DEV).float().to(torch.float8_e4m3fn)
+    w = torch.randint(-2, 3, (m, k), generator=g, device=DEV).float().to(torch.float8_e4m3fn)
+    xs = torch.exp2(torch.randint(0, 3, (n, kb), generator=g, device=DEV).float())
+    ws = torch.exp2(torch.randint(-2, 1, (mb, kb), generator=g, device=DEV).float())
+    y = sga.gemm_fp8(x, xs, w, ws)
+    X = x.double() * xs.double().repeat_interleave(128, 1)[:, :k]
+    W = w.double() * ws.double().repeat_interleave(128, 0)[:m].repeat_interleave(128, 1)[:, :k]
+    assert torch.equal(y.double(), X @ W.T)
+
+
+@pytest.mark.parametrize("n,m,k", [(8, 2304, 7168), (100, 1000, 3000 // 16 * 16), (260, 390, 2064)])
+def test_product_repeats_bit_for_bit_and_leaves_its_workspace_ready(n, m, k):
+    x, xs, w, wsc = product_case(n, m, k, 3)
+    ws = sga.alloc_gemm_fp8_workspace()
+    first = sga.gemm_fp8(x, xs, w, wsc, ws=ws)
+    for _ in range(5):
+        assert torch.equal(sga.gemm_fp8(x, xs, w, wsc, ws=ws), first)
+    assert int(ws[:1280].to(torch.int64).sum()) == 0  # status and counters
+    check_product(n + 1, m, k, torch.bfloat16, seed=9, ws=ws)  # other sizes, same workspace
+
+
+def test_product_propagates_nan_and_infinite_scales_to_their_rows_only():
+    x, xs, w, wsc = product_case(20, 200, 400, 4)
+    x[3, 7] = 0x7F
+    xs[5, 1] = float("inf")
+    w[9, 30] = 0xFF
+    y = sga.gemm_fp8(x, xs, w, wsc)
+    bad = ~torch.isfinite(y)
+    assert bool(bad[3].all()) and bool(bad[5].all()) and bool(bad[:, 9].all())
+    keep = torch.ones_like(bad)
+    keep[3] = keep[5] = False
+    keep[:, 9] = False
+    assert not bool((bad & keep).any())
+
+
+def test_product_leading_dims_and_out():
+    x, xs, w, wsc = product_case(6, 96, 256, 5)
+    want = sga.gemm_fp8(x, xs, w, wsc, out_dtype=torch.bfloat16)
+    out = torch.empty((2, 3, 96), dtype=torch.bfloat16, device=DEV)
+    got = sga.gemm_fp8(x.view(2, 3, 256), xs.view(2, 3, 2), w.view(torch.float8_e4m3fn), wsc, out=out)
+    assert got is out and torch.equal(out.view(6, 96), want)
+
+
+# ------------------------------------------------------------------------------------------------ 4-bit cache rows
+def check_append(rows, pos, L):
+    B, T = pos.shape
+    g = gen(77)
+    cache = torch.randint(0, 256, (B, L, 416), generator=g, device=DEV, dtype=torch.int32).to(torch.uint8)
+    before = cache.clone()
+    ws = status_ws()
+    assert sga.kv4_append(rows, pos, cache, ws=ws) is cache
+    assert sga.device_status(ws) == 0
+    code, scale, _ = lowbit.kv4_pack(lowbit.to_f64(rows).reshape(B * T, 576))
+    got = torch.stack([cache[b, p] for b in range(B) for p in pos[b].tolist()]).cpu().numpy()
+    byte = got[:, :256]
+    np.testing.assert_array_equal(np.stack([byte & 15, byte >> 4], -1).reshape(B * T, 512), code)
+    np.testing.assert_array_equal(got[:, 256:288], scale)
+    np.testing.assert_array_equal(got[:, 288:], u8(rows[..., 512:].contiguous()).reshape(B * T, 128))
+    kept = torch.ones((B, L), dtype=torch.bool)
+    for b in range(B):
+        kept[b, pos[b].long().cpu()] = False
+    kept = kept.to(DEV)
+    assert torch.equal(cache[kept], before[kept])
+    values = sga.kv4_read(cache, pos, ws=ws)
+    want = lowbit.kv4_values(got).reshape(B, T, 576)
+    np.testing.assert_array_equal(lowbit.to_f64(values), want)
+    return cache
+
+
+@pytest.mark.parametrize("B,T,L", [(1, 1, 1), (2, 1, 50), (3, 7, 40), (1, 1000, 1003)])
+def test_append_and_read_match_definition(B, T, L):
+    g = gen(B + T)
+    rows = randn(g, B, T, 576) * torch.exp2(torch.randint(-8, 11, (B, T, 1), generator=g, device=DEV).float())
+    pos = torch.stack([torch.randperm(L, generator=g, device=DEV)[:T] for _ in range(B)]).to(torch.int32)
+    check_append(rows.to(torch.bfloat16), pos, L)
+
+
+def test_append_special_values():
+    """Zeros of both signs, saturating and vanishing groups, rounding ties of codes and scales, infinities, NaN."""
+    rows = torch.zeros((1, 6, 576), dtype=torch.float64)
+    rows[0, 0, 16:32] = -0.0
+    rows[0, 1, :16] = torch.tensor([6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, -6, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5])
+    rows[0, 1, 16:32] = rows[0, 1, :16] * 2.0 ** -8
+    rows[0, 2, :16] = torch.linspace(-5000, 5000, 16)
+    rows[0, 2, 16:32] = 6 * 2.0 ** -10  # amax / 6 is half the smallest scale: a tie, to zero
+    rows[0, 2, 32:48] = 6 * 2.0 ** -10 * (1 + 2.0 ** -7)
+    rows[0, 2, 48] = 6 * 17 / 16  # scale 1.0625: a tie between 1 and 1.125
+    rows[0, 3, 5], rows[0, 3, 6], rows[0, 3, 7] = float("inf"), -float("inf"), 3.0
+    rows[0, 4, 100] = 2.0 ** -130
+    rows[0, 4, 512:] = torch.linspace(-1e30, 1e30, 64)
+    rows[0, 5, :] = 1.0
+    check_append(rows.to(torch.bfloat16).to(DEV), torch.tensor([[5, 0, 3, 1, 2, 4]], dtype=torch.int32, device=DEV), 7)
+
+
+def test_append_nan_marks_its_group():
+    rows = torch.ones((1, 1, 576), dtype=torch.bfloat16, device=DEV)
+    rows[0, 0, 40] = float("nan")
+    cache = torch.zeros((1, 1, 416), dtype=torch.uint8, device=DEV)
+    pos = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    got = sga.kv4_read(sga.kv4_append(rows, pos, cache), pos)[0, 0]
+    assert bool(torch.isnan(got[32:48]).all()) and not bool(torch.isnan(got[:32]).any() | torch.isnan(got[48:]).any())
+
+
+def test_cache_positions_out_of_range_are_reported_and_skipped():
+    rows = randn(gen(1), 2, 3, 576).to(torch.bfloat16)
+    cache = torch.zeros((2, 10, 416), dtype=torch.uint8, device=DEV)
+    ws = status_ws()
+    sga.kv4_append(rows, torch.tensor([[0, 10, -1], [9, 1, 2]], dtype=torch.int32, device=DEV), cache, ws=ws)
+    assert sga.device_status(ws) == 6
+    written = cache.to(torch.int32).sum(-1) > 0
+    assert written.nonzero().tolist() == [[0, 0], [1, 1], [1, 2], [1, 9]]
+    ws = status_ws()
+    got = sga.kv4_read(cache, torch.tensor([[0, -1, -1], [9, 9, -1]], dtype=torch.int32, device=DEV), ws=ws)
+    assert sga.device_status(ws) == 0
+    assert not bool(got[0, 1:].any()) and torch.equal(got[1, 0], got[1, 1]) and bool(got[1, 0].any())
+    got = sga.kv4_read(cache, torch.tensor([[0, -2, 0], [10, 9, 1]], dtype=torch.int32, device=DEV), ws=ws)
+    assert sga.device_status(ws) == 6
+    assert not bool(got[0, 1].any()) and not bool(got[1, 0].any())
+
+
+# ------------------------------------------------------------------------------------------------ attention
+def fill_cache(g, B, L):
+    rows = randn(g, B, L, 576).to(torch.bfloat16)
+    cache = torch.zeros((B, L, 416), dtype=torch.uint8, device=DEV)
+    pos = torch.arange(L, dtype=torch.int32, device=DEV).repeat(B, 1)
+    return sga.kv4_append(rows, pos, cache)
+
+
+def check_attend(q, cache, idx, gate, out=None):
+    ws = status_ws()
+    got = sga.sparse_mla_attend_kv4(q, cache, idx, gate, ws=ws, out=out)
+    assert got.dtype == torch.bfloat16 and sga.device_status(ws) == 0
+    want, spread, zabs, total = lowbit.attend_kv4(lowbit.to_f64(q), cache.cpu().numpy(), idx.cpu().numpy(),
+                                           None if gate is None else lowbit.to_f64(gate))
+    err = np.abs(lowbit.to_f64(got) - want)
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2 * 41 * 2.0 ** -23 * zabs) * spread * (1 + 2.0 ** -8)
+    tol += 2.0 ** -32 * total
+    assert (err <= tol).all(), f"max error / bound {(err / np.maximum(tol, 1e-300)).max():.3f}"
+    return got
+
+
+def pick(g, B, T, L, K, fill=1.0):
+    """Distinct positions in random order, -1 in the rest of the slots."""
+    idx = torch.full((B, T, K), -1, dtype=torch.int32, device=DEV)
+    for b in range(B):
+        for t in range(T):
+            n = min(L, K) if fill == 1.0 else int(min(L, K) * fill)
+            slots = torch.randperm(K, generator=g, device=DEV)[:n]
+            idx[b, t, slots] = torch.randperm(L, generator=g, device=DEV)[:n].to(torch.int32)
+    return idx
+
+
+ATTEND_CASES = [(1, 1, 64, 64, 1.0), (1, 1, 1, 64, 1.0), (2, 1, 3000, 2048, 1.0), (1, 3, 700, 128, 0.5),
+                (3, 2, 300, 192, 1.0), (20, 1, 500, 320, 0.7), (2, 5, 1001, 1088, 0.9), (40, 4, 200, 256, 0.8),
+                (1, 150, 400, 128, 1.0)]
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("B,T,L,K,fill", ATTEND_CASES)
+def test_attend_kv4_matches_definition(B, T, L, K, fill, gated):
+    g = gen(B * 100 + T * 10 + K)
+    cache = fill_cache(g, B, L)
+    q = randn(g, B, T, 64, 576).to(torch.bfloat16)
+    gate = randn(g, B, T, 64).to(torch.bfloat16) if gated else None
+    check_attend(q, cache, pick(g, B, T, L, K, fill), gate)
+
+
+def test_attend_kv4_empty_and_sparse_rows():
+    """A query with nothing selected gives zeros; one valid slot in the last chunk; duplicates count twice."""
+    g = gen(8)
+    cache = fill_cache(g, 1, 100)
+    q = randn(g, 1, 4, 64, 576).to(torch.bfloat16)
+    idx = torch.full((1, 4, 512), -1, dtype=torch.int32, device=DEV)
+    idx[0, 1, 511] = 99
+    idx[0, 2, ::7] = 5
+    idx[0, 2, 3] = 6
+    idx[0, 3, 64:128] = torch.arange(64, dtype=torch.int32, device=DEV)
+    got = check_attend(q, cache, idx, None)
+    assert not bool(got[0, 0].any())
+
+
+def test_attend_kv4_does_not_read_unselected_rows():
+    """Every row that is not selected holds NaN scales, NaN rope and all-ones codes; row 0 among them."""
+    g = gen(9)
+    cache = fill_cache(g, 2, 400)
+    idx = pick(g, 2, 2, 399, 256, 0.6)
+    idx = torch.where(idx >= 0, idx + 1, idx)
+    q = randn(g, 2, 2, 64, 576).to(torch.bfloat16)
+    used = torch.zeros((2, 400), dtype=torch.bool, device=DEV)
+    for b in range(2):
+        used[b, idx[b][idx[b] >= 0].long()] = True
+    cache[~used] = 0xFF
+    check_attend(q, cache, idx, None)
+
+
+def test_attend_kv4_wide_range_of_logits_and_query_sizes():
+    """The running maximum grows from chunk to chunk; heads scaled from 2^-80 to 2^60, one of zeros."""
+    g = gen(10)
+    B, L, K = 1, 640, 640
+    rows = randn(g, B, L, 576)
+    rows *= torch.linspace(0.05, 6, L, device=DEV)[None, :, None]
+    cache = torch.zeros((B, L, 416), dtype=torch.uint8, device=DEV)
+    idx = torch.arange(L, dtype=torch.int32, device=DEV).view(1, 1, K).contiguous()
+    sga.kv4_append(rows.to(torch.bfloat16), idx[0], cache)
+    q = randn(g, 1, 1, 64, 576)
+    check_attend(q.to(torch.bfloat16), cache, idx, None)
+    scale = torch.exp2(torch.linspace(-80, 0, 64, device=DEV).round())
+    scale[7] = 0.0
+    check_attend((q * scale[None, None, :, None]).to(torch.bfloat16), cache, idx, None)
+    # logits of +-2^60: one row takes all the weight, and the largest logit decides it
+    big = (q * 2.0 ** 60).to(torch.bfloat16)
+    got = sga.sparse_mla_attend_kv4(big, cache, idx)
+    values = torch.tensor(lowbit.kv4_values(cache[0].cpu().numpy()), device=DEV)
+    best = (big[0, 0].double() @ values.T).argmax(-1)
+    assert torch.equal(got[0, 0].double(), values[best, :512])
+
+
+def test_attend_kv4_nan_in_a_selected_row_shows():
+    g = gen(11)
+    cache = fill_cache(g, 1, 64)
+    cache[0, 3, 256:288] = 0x7F
+    idx = torch.arange(64, dtype=torch.int32, device=DEV).view(1, 1, 64).contiguous()
+    q = randn(g, 1, 1, 64, 576).to(torch.bfloat16)
+    assert bool(torch.isnan(sga.sparse_mla_attend_kv4(q, cache, idx)).all())
+
+
+def test_attend_kv4_index_out_of_range_is_reported_and_left_out():
+    g = gen(12)
+    cache = fill_cache(g, 2, 50)
+    q = randn(g, 2, 1, 64, 576).to(torch.bfloat16)
+    idx = pick(g, 2, 1, 50, 64)
+    bad = idx.clone()
+    bad[0, 0, bad[0, 0] < 0] = 50
+    bad[1, 0, 5] = -7
+    ws = status_ws()
+    got = sga.sparse_mla_attend_kv4(q, cache, bad, ws=ws)
+    assert sga.device_status(ws) == 6
+    idx[1, 0, 5] = -1
+    assert torch.equal(got, sga.sparse_mla_attend_kv4(q, cache, idx))
+
+
+def test_attend_kv4_offsets_past_32_bits():
+    """A cache of over 4 GiB: rows near its end, through append, read and attention."""
+    g = gen(13)
+    L = 10_500_000
+    cache = torch.zeros((1, L, 416), dtype=torch.uint8, device=DEV)
+    n = 300
+    pos = (L - 1 - torch.randperm(200_000, generator=g, device=DEV)[:n]).to(torch.int32).view(1, n)
+    rows = randn(g, 1, n, 576).to(torch.bfloat16)
+    sga.kv4_append(rows, pos, cache)
+    small = torch.zeros((1, n, 416), dtype=torch.uint8, device=DEV)
+    order = torch.arange(n, dtype=torch.int32, device=DEV).view(1, n)
+    sga.kv4_append(rows, order, small)
+    assert torch.equal(sga.kv4_read(cache, pos), sga.kv4_read(small, order))
+    q = randn(g, 1, 1, 64, 576).to(torch.bfloat16)
+    pad = torch.full((1, 1, 320 - n), -1, dtype=torch.int32, device=DEV)
+    a = sga.sparse_mla_attend_kv4(q, cache, torch.cat((pos.view(1, 1, n), pad), -1).contiguous())
+    b = sga.sparse_mla_attend_kv4(q, small, torch.cat((order.view(1, 1, n), pad), -1).contiguous())
+    assert torch.equal(a, b)
+
+
+def test_attend_kv4_writes_its_rows_only_and_repeats():
+    g = gen(14)
+    cache = fill_cache(g, 2, 500)
+    q = randn(g, 2, 3, 64, 576).to(torch.bfloat16)
+    idx = pick(g, 2, 3, 500, 448)
+    room = torch.full((4, 3, 64, 512), 7.0, dtype=torch.bfloat16, device=DEV)
+    first = check_attend(q, cache, idx, None, out=room[1:3]).clone()
+    assert bool((room[0] == 7).all()) and bool((room[3] == 7).all())
+    for _ in range(5):
+        assert torch.equal(sga.sparse_mla_attend_kv4(q, cache, idx), first)
+
+
+# ------------------------------------------------------------------------------------------------ together
+def test_forward_kv4_selects_as_forward_and_attends_over_the_cache():
+    for B, T, L in [(3, 1, 3000), (1, 9, 2500)]:
+        wl = synth.custom(batch=B, n_q=T, ctx=L)
+        x = synth.make_inputs(wl, device=DEV, seed=3)
+        pos = torch.arange(L, dtype=torch.int32, device=DEV).repeat(B, 1)
+        cache = sga.kv4_append(x["kv"], pos, torch.zeros((B, L, 416), dtype=torch.uint8, device=DEV))
+        want_idx, _ = sga.forward(x["q_idx"], x["w"], x["k_idx"], x["q"], x["kv"], x["gate"], x["q_pos"])
+        ws = sga.alloc_workspace(sga.make_dims(B, T, L))
+        for _ in range(2):  # the workspace is ready for the next call
+            idx, out = sga.forward_kv4(x["q_idx"], x["w"], x["k_idx"], x["q"], cache, x["gate"], x["q_pos"], ws=ws)
+            assert sga.device_status(ws) == 0
+            assert torch.equal(idx, want_idx)
+            assert torch.equal(out, sga.sparse_mla_attend_kv4(x["q"], cache, idx, x["gate"]))
+        _, out2 = sga.forward_kv4(x["q_idx"], x["w"], x["k_idx"], x["q"], cache, x["gate"], x["q_pos"], ws=ws,
+                                  return_idx=False)
+        assert torch.equal(out, out2)
+
+
+def test_calls_on_another_stream_and_in_a_graph():
+    """Each call captured once on a side stream and replayed on new inputs gives what an eager call gives."""
+    g = gen(15)
+    x = randn(g, 5, 512).to(torch.bfloat16)
+    w, wsc = rand_codes(g, 300, 512), torch.rand((3, 4), generator=g, device=DEV) + 0.5
+    ws = sga.alloc_gemm_fp8_workspace()
+    rows = randn(g, 2, 1, 576).to(torch.bfloat16)
+    cache = fill_cache(g, 2, 200)
+    pos = torch.tensor([[3], [199]], dtype=torch.int32, device=DEV)
+    q = randn(g, 2, 1, 64, 576).to(torch.bfloat16)
+    idx = pick(g, 2, 1, 200, 192)
+    ws2 = status_ws()
+
+    def step():
+        codes, scale = sga.quantize_fp8(x)
+        y = sga.gemm_fp8(codes, scale, w, wsc, ws=ws)
+        sga.kv4_append(rows, pos, cache, ws=ws2)
+        return y, sga.kv4_read(cache, pos, ws=ws2), sga.sparse_mla_attend_kv4(q, cache, idx, ws=ws2)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step()
+    for seed in (1, 2):
+        h = gen(seed)
+        x.copy_(randn(h, 5, 512))
+        rows.copy_(randn(h, 2, 1, 576))
+        q.copy_(randn(h, 2, 1, 64, 576))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in got]
+        for a, b in zip(replayed, step()):
+            assert torch.equal(a, b)
+    assert sga.device_status(ws) == 0 and sga.device_status(ws2) == 0
+
+
+def test_two_streams_at_once_with_their_own_workspaces():
+    cases = [product_case(40, 2304, 1536, 21), product_case(200, 1000, 2048, 22)]
+    want = [sga.gemm_fp8(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [sga.alloc_gemm_fp8_workspace() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(sga.gemm_fp8(*cases[i], ws=spaces[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y in outs[i]:
+            assert torch.equal(y, want[i])
+
+
+# ------------------------------------------------------------------------------------------------ refusals
+def test_python_refusals():
+    x, xs, w, wsc = product_case(4, 64, 256, 30)
+    with pytest.raises(TypeError):
+        sga.gemm_fp8(x, xs, w, wsc, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        sga.gemm_fp8(x, xs[:, :1].contiguous(), w, wsc)
+    with pytest.raises(ValueError):
+        sga.gemm_fp8(x[:, ::2], xs, w, wsc)
+    with pytest.raises(ValueError):
+        sga.gemm_fp8(x.cpu(), xs, w, wsc)
+    with pytest.raises(sga.SGAError):  # k not a multiple of 16
+        sga.gemm_fp8(x[:, :24].contiguous(), xs[:, :1].contiguous(), w[:, :24].contiguous(), wsc[:, :1].contiguous())
+    with pytest.raises(sga.SGAError):  # workspace too small
+        sga.gemm_fp8(x, xs, w, wsc, ws=status_ws())
+    with pytest.raises(TypeError):
+        sga.quantize_fp8(torch.zeros((2, 32), device=DEV))
+    with pytest.raises(sga.SGAError):
+        sga.quantize_fp8(torch.zeros((2, 24), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError):
+        sga.quantize_fp8(torch.zeros((0, 32), dtype=torch.bfloat16, device=DEV))
+    cache = torch.zeros((1, 10, 416), dtype=torch.uint8, device=DEV)
+    q = torch.zeros((1, 1, 64, 576), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        sga.sparse_mla_attend_kv4(q, cache[:, :, :400].contiguous(), torch.zeros((1, 1, 64), dtype=torch.int32, device=DEV))
+    with pytest.raises(sga.SGAError):  # K not a multiple of 64
+        sga.sparse_mla_attend_kv4(q, cache, torch.zeros((1, 1, 65), dtype=torch.int32, device=DEV))
