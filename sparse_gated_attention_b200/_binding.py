@@ -47,7 +47,7 @@ KV4_ROW_BYTES = 416  # one row of the 4-bit latent cache (see sga_kv4_append)
 FP8_BLOCK = 128  # channels (and weight rows) that share a scale
 GEMM_FP8_WORKSPACE_BYTES = 24 * 1024 * 1024
 STATUS_BYTES = 256  # the workspace of a call that keeps only its status word there
-OUT_FP32, OUT_BF16 = 0, 1
+_OUT_TYPES = {torch.float32: 0, torch.bfloat16: 1}  # sga_out_type_t
 
 
 class SGAError(RuntimeError):
@@ -126,17 +126,22 @@ def _check(call: str, status: int) -> None:
         raise SGAError(call, status)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
+    """The handle of `stream`, or of the current stream of the current device."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, dtype, shape=None):
+    # one test when all is well: the calls of a decode step are as short as their launches
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.device.type != "cuda":
@@ -152,16 +157,16 @@ def _need(t, name, dtype, shape=None):
 
 def _one_device(*tensors):
     """Every given tensor lives on the current CUDA device: the library launches there, on its streams."""
-    dev = torch.device("cuda", torch.cuda.current_device())
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"expected every tensor on the current device {dev}, got one on {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected every tensor on the current device cuda:{dev}, got one on {t.device}")
 
 
 def _need_fp8(t, name, shape):
-    """An E4M3 tensor (torch.float8_e4m3fn, or its bytes as uint8), returned as uint8."""
+    """An E4M3 tensor: torch.float8_e4m3fn, or its bytes as uint8."""
     if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
+        return _need(t, name, torch.float8_e4m3fn, shape)  # the library takes its address: no view is needed
     return _need(t, name, torch.uint8, shape)
 
 
@@ -374,7 +379,8 @@ def kv4_read(kv4, pos, kv_rows=None, ws=None, stream=None):
     _need(pos, "pos", torch.int32, (B, T))
     if kv_rows is None:
         kv_rows = torch.empty((B, T, QK_DIM), dtype=torch.bfloat16, device=kv4.device)
-    _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
+    else:
+        _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
     dims = make_dims(B, T, L)
     ws = _status_ws(ws, kv4.device)
     _one_device(kv4, pos, kv_rows, ws)
@@ -396,7 +402,8 @@ def sparse_mla_attend_kv4(q, kv4, idx, gate=None, out=None, ws=None, stream=None
     dims = make_dims(B, T, L, K)
     if out is None:
         out = torch.empty((B, T, HEADS, V_DIM), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
+    else:
+        _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
     ws = _status_ws(ws, q.device)
     _one_device(q, kv4, idx, gate, out, ws)
     _check("sga_sparse_mla_attend_kv4", load_library().sga_sparse_mla_attend_kv4(
@@ -441,18 +448,22 @@ def quantize_fp8(x, codes=None, scale=None, stream=None):
     """bf16 activations x [..., K] -> (codes [..., K] float8_e4m3fn, scale [..., ceil(K / 128)] fp32): one
     power-of-two scale for each token and block of 128 channels (sga_quantize_fp8)."""
     _need(x, "x", torch.bfloat16)
-    if x.dim() < 1 or x.numel() == 0:
-        raise ValueError("x: must have at least one element")
-    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    shape, n = x.shape, x.numel()
+    if n == 0 or not shape:
+        raise ValueError("x: must be [..., K] with at least one element")
+    K = shape[-1]
+    s_shape = (*shape[:-1], -(-K // FP8_BLOCK))
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    _need_fp8(codes, "codes", x.shape)
+        codes = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _need_fp8(codes, "codes", shape)
     if scale is None:
-        scale = torch.empty((*lead, -(-K // FP8_BLOCK)), dtype=torch.float32, device=x.device)
-    _need(scale, "scale", torch.float32, (*lead, -(-K // FP8_BLOCK)))
+        scale = torch.empty(s_shape, dtype=torch.float32, device=x.device)
+    else:
+        _need(scale, "scale", torch.float32, s_shape)
     _one_device(x, codes, scale)
     _check("sga_quantize_fp8", load_library().sga_quantize_fp8(
-        x.numel() // K, K, _ptr(x), _ptr(codes), _ptr(scale), _stream(stream)))
+        n // K, K, _ptr(x), _ptr(codes), _ptr(scale), _stream(stream)))
     return codes, scale
 
 
@@ -467,27 +478,30 @@ def gemm_fp8(x, x_scale, w, w_scale, out_dtype=torch.float32, out=None, ws=None,
     if not isinstance(w, torch.Tensor) or w.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x: expected [..., K] and w: [M, K]")
     M, K = w.shape
-    lead = tuple(x.shape[:-1])
+    lead = x.shape[:-1]
     kb = -(-K // FP8_BLOCK)
-    x = _need_fp8(x, "x", (*lead, K))
-    w = _need_fp8(w, "w", (M, K))
+    _need_fp8(x, "x", (*lead, K))
+    _need_fp8(w, "w", (M, K))
     _need(x_scale, "x_scale", torch.float32, (*lead, kb))
     _need(w_scale, "w_scale", torch.float32, (-(-M // FP8_BLOCK), kb))
-    if out is not None:
-        out_dtype = out.dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
-    if x.numel() == 0 or M == 0:
+    n = x.numel()
+    if n == 0 or M == 0:
         raise ValueError("x, w: must have at least one element")
     if out is None:
+        if out_dtype not in _OUT_TYPES:
+            raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
         out = torch.empty((*lead, M), dtype=out_dtype, device=x.device)
-    _need(out, "out", out_dtype, (*lead, M))
+    else:
+        out_dtype = out.dtype
+        if out_dtype not in _OUT_TYPES:
+            raise TypeError(f"out: expected torch.float32 or torch.bfloat16, got {out_dtype}")
+        _need(out, "out", out_dtype, (*lead, M))
     if ws is None:
         ws = alloc_gemm_fp8_workspace(x.device)
     _one_device(x, x_scale, w, w_scale, out, ws)
     _check("sga_gemm_fp8", load_library().sga_gemm_fp8(
-        x.numel() // K, M, K, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(out),
-        OUT_BF16 if out_dtype == torch.bfloat16 else OUT_FP32, _ptr(ws), ws.numel(), _stream(stream)))
+        n // K, M, K, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(out), _OUT_TYPES[out_dtype], _ptr(ws),
+        ws.numel(), _stream(stream)))
     return out
 
 

@@ -7,8 +7,8 @@
 //
 // What differs from the bf16 kernel follows from the row being 2.8 times smaller:
 //   * A chunk's 64 rows are 26 KB, so they are gathered into registers: eight
-//     producer warps hold the next chunk's codes while they expand the current
-//     one, and the whole value ring in shared memory is left to expanded tiles.
+//     producer warps hold the next chunk's codes while they store the current
+//     one's expanded tiles, and the whole value ring in shared memory is left to expanded tiles.
 //   * A code times its scale has at most 6 significant bits between 2^-10 and
 //     2,688, so it is exact in fp16 (and in bf16).  The tiles hold fp16: two
 //     codes expand with one conversion and one multiplication, and P can be one
@@ -53,13 +53,12 @@ constexpr int kMaskRing = 4;
 constexpr int kProducerWarps = 8;            // warps 0-7: four threads per chunk row
 constexpr int kMmaWarp = 8;
 constexpr int kSoftmaxThreads = 128;         // warps 9-12
-constexpr int kPvThread = (kMmaWarp + 1) * 32;  // the softmax thread that issues PV
 constexpr int kThreads = 32 * (kMmaWarp + 1) + kSoftmaxThreads;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;
 // barriers: pair_full[8] pair_empty[8] rope_full[2] rope_empty[2] q_full s_full[2] s_free[2]
-//           qk_done p_free o_full mask_full[4] mask_empty[4]
-constexpr int kNumBars = 2 * kPairRing + 2 * kRopeRing + 1 + 2 + 2 + 3 + 2 * kMaskRing;
+//           p_full p_free o_full
+constexpr int kNumBars = 2 * kPairRing + 2 * kRopeRing + 1 + 2 + 2 + 3;
 constexpr int kMaxSplits = 8;                // splits of a query = CTAs of its cluster
 constexpr size_t kSmemBytes = 1024 + kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes + kPBytes +
                               kNumBars * 8 + kMaskRing * 8 + 2 * kHeads * 4 + kHeads * 8 + 16;
@@ -121,6 +120,13 @@ __device__ __forceinline__ uint2 ld_row8(const uint8_t* p) {
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// Four 8 x 8 blocks of 16-bit values in the fragment layout, to the rows whose addresses lanes 0-31 give.
+__device__ __forceinline__ void stmatrix_x4(uint32_t row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(a), "r"(b), "r"(c),
+               "r"(d)
                : "memory");
 }
 
@@ -196,11 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
   const uint32_t q_full = bar0 + 8u * (2 * kPairRing + 2 * kRopeRing);
   auto s_full = [&](int b) { return q_full + 8u * (1 + b); };
   auto s_free = [&](int b) { return q_full + 8u * (3 + b); };
-  const uint32_t qk_done = q_full + 8u * 5;  // every QK^T MMA of the MMA warp has finished
+  const uint32_t p_full = q_full + 8u * 5;
   const uint32_t p_free = q_full + 8u * 6;
-  const uint32_t o_full = q_full + 8u * 7;
-  auto mask_full = [&](int b) { return q_full + 8u * (8 + b); };
-  auto mask_empty = [&](int b) { return q_full + 8u * (8 + kMaskRing + b); };
+  const uint32_t o_full = q_full + 8u * 7;  // every MMA has finished
   uint64_t* masks = bars + kNumBars;
   float* head_f = reinterpret_cast<float*>(masks + kMaskRing);  // [64] per-head factors
   float* q_scale = head_f + kHeads;                              // [64] softmax scale (log2) of the scaled heads
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(own_ml + kHeads);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
   cg::cluster_group cluster = cg::this_cluster();
   const int row = blockIdx.x / p.splits;
@@ -229,15 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     mbar_init(q_full, kProducerWarps);
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
-      mbar_init(s_free(b), kSoftmaxThreads);
+      mbar_init(s_free(b), kSoftmaxThreads / 32);
     }
-    mbar_init(qk_done, 1);
+    mbar_init(p_full, kSoftmaxThreads / 32);
     mbar_init(p_free, 1);
     mbar_init(o_full, 1);
-    for (int b = 0; b < kMaskRing; ++b) {
-      mbar_init(mask_full(b), kProducerWarps);
-      mbar_init(mask_empty(b), kSoftmaxThreads);
-    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -262,21 +262,22 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     const int r = ptid >> 2;    // this thread's row of the chunk
     const int part = ptid & 3;  // and its quarter of that row
     bool ok = true;
+    // Indices are fetched two chunks ahead and looked at only when the rows are loaded, one chunk ahead (into the
+    // registers that the chunk's expansion has just left).
     auto load_idx = [&](int j) {
-      if (j >= nchunks) return -1;
-      const int v = __ldg(idx_row + slot_base + j * kChunk + r);  // K is a multiple of 64: a chunk has no tail
-      if (v < -1 || v >= p.kv_stride) {
-        record_status(p.status, kStatusDeviceArg);
-        return -1;
-      }
-      return v;
+      // K is a multiple of 64: a chunk has no tail
+      return j < nchunks ? __ldg(idx_row + slot_base + j * kChunk + r) : -1;
     };
     auto load = [&](RowPart& d, int v) {
-      load_row(d, kv_b + static_cast<size_t>(v < 0 ? 0 : v) * kRowBytes, part, v >= 0);
+      const bool valid = v >= 0 && v < p.kv_stride;
+      if (!valid && v != -1) record_status(p.status, kStatusDeviceArg);
+      load_row(d, kv_b + static_cast<size_t>(valid ? v : 0) * kRowBytes, part, valid);
+      return valid;
     };
-    int cur_idx = load_idx(0), next_idx = load_idx(1);
-    RowPart next;
-    load(next, cur_idx);
+    const int first_idx = load_idx(0);
+    int ahead_idx = load_idx(1);
+    RowPart cur;
+    bool cur_valid;
     {
       // Q: four threads per head, 16-byte pieces part, part + 4, ...; pieces 64.. are the rope dims
       const int h = r;
@@ -284,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       uint4 v[kQPieces / 4];
 #pragma unroll
       for (int i = 0; i < kQPieces / 4; ++i) v[i] = ld_row16(q_row + 16 * (part + 4 * i));
+      cur_valid = load(cur, first_idx);
       uint32_t top = 0;  // largest magnitude as bf16 bits
 #pragma unroll
       for (int i = 0; i < kQPieces / 4; ++i) {
@@ -315,55 +317,19 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
-    for (int j = 0; j < nchunks; ++j) {
-      const RowPart cur = next;
-      const uint32_t seen = __ballot_sync(0xFFFFFFFFu, cur_idx >= 0);
-      if (j + 1 < nchunks) {
-        cur_idx = next_idx;
-        load(next, cur_idx);
-        next_idx = load_idx(j + 2);
-      }
-      {
-        // validity of the warp's eight rows (every fourth ballot bit) -> bits 8 warp .. of the chunk's mask
-        uint32_t m = seen & 0x11111111u;
-        m = (m | (m >> 3)) & 0x03030303u;
-        m = (m | (m >> 6)) & 0x000F000Fu;
-        m = (m | (m >> 12)) & 0xFFu;
-        if (lane == 0) {
-          const int mb = j % kMaskRing;
-          if (mbar_wait(mask_empty(mb), static_cast<uint32_t>((j / kMaskRing) & 1) ^ 1u, abort_flag)) {
-            reinterpret_cast<uint8_t*>(masks + mb)[warp] = static_cast<uint8_t>(m);
-            mbar_arrive(mask_full(mb));
-          } else {
-            ok = false;
-          }
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-      }
-      const int rs = j % kRopeRing;
-      ok = mbar_wait(rope_empty(rs), static_cast<uint32_t>((j / kRopeRing) & 1) ^ 1u, abort_flag);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+    // This thread's 32 dims of a pair are four 16-byte columns of box part / 2.  The upper box's threads take their
+    // words in the order 2, 3, 0, 1, so the eight threads of a store phase reach eight different columns.
+    const uint32_t flip = part & 2;
+    const uint32_t dst0 = pairs + (part >> 1) * kBoxBytes + r * 128;
+    uint32_t col[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        st_shared16(rope + rs * kBoxBytes + r * 128 + (((2 * part + i) ^ (r & 7)) << 4), cur.rope[i]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(rope_full(rs));
-      // value dims 128 q .. 128 q + 127 -> pair slot (4 j + q) mod 8; this thread's 32 dims are four
-      // 16-byte columns of box part / 2.  The upper box's threads store their columns in the order
-      // 2, 3, 0, 1, so the eight threads of a store phase reach eight different columns.
-      const uint32_t flip = part & 2;
-      const uint32_t dst0 = (part >> 1) * kBoxBytes + r * 128;
-      const uint32_t col0 = (part & 1) * 4;
+    for (int i = 0; i < 4; ++i) col[i] = ((((part & 1) * 4) + (i ^ flip)) ^ (r & 7)) << 4;
+    for (int j = 0; j < nchunks; ++j) {
+      // The chunk is expanded in registers before its slots are free, so that only the stores stand between PV(j - 2)
+      // and QK^T(j).
+      uint4 tile[kPairsPerChunk][4];
 #pragma unroll
       for (int q = 0; q < kPairsPerChunk; ++q) {
-        const int n = j * kPairsPerChunk + q;
-        const int slot = n % kPairRing;
-        ok = mbar_wait(pair_empty(slot), static_cast<uint32_t>((n / kPairRing) & 1) ^ 1u, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
         // the scales of pair q are with thread q of the row's four; this thread's two are its half word `part`
         const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, cur.scales.x, (lane & ~3) + q);
         const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, cur.scales.y, (lane & ~3) + q);
@@ -371,13 +337,47 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         uint32_t s0, s1;
         expand_scales(two & 0xFFFFu, s0, s1);
         const uint4 c = cur.codes[q];
-        const uint32_t a0 = flip ? c.z : c.x, a1 = flip ? c.w : c.y, a2 = flip ? c.x : c.z, a3 = flip ? c.y : c.w;
         const uint32_t sa = flip ? s1 : s0, sb = flip ? s0 : s1;
-        const uint32_t base = pairs + slot * kPairBytes + dst0;
-        st_shared16(base + (((col0 + flip) ^ (r & 7)) << 4), expand_codes(a0, sa));
-        st_shared16(base + (((col0 + (1 ^ flip)) ^ (r & 7)) << 4), expand_codes(a1, sa));
-        st_shared16(base + (((col0 + (2 ^ flip)) ^ (r & 7)) << 4), expand_codes(a2, sb));
-        st_shared16(base + (((col0 + (3 ^ flip)) ^ (r & 7)) << 4), expand_codes(a3, sb));
+        tile[q][0] = expand_codes(flip ? c.z : c.x, sa);
+        tile[q][1] = expand_codes(flip ? c.w : c.y, sa);
+        tile[q][2] = expand_codes(flip ? c.x : c.z, sb);
+        tile[q][3] = expand_codes(flip ? c.y : c.w, sb);
+      }
+      const uint32_t seen = __ballot_sync(0xFFFFFFFFu, cur_valid);
+      const int rs = j % kRopeRing;
+      ok = mbar_wait(rope_empty(rs), static_cast<uint32_t>((j / kRopeRing) & 1) ^ 1u, abort_flag);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        st_shared16(rope + rs * kBoxBytes + r * 128 + (((2 * part + i) ^ (r & 7)) << 4), cur.rope[i]);
+      if (j + 1 < nchunks) {
+        cur_valid = load(cur, ahead_idx);
+        ahead_idx = load_idx(j + 2);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        // Validity of the warp's eight rows (every fourth ballot bit) -> bits 8 warp .. of the chunk's mask, which
+        // the softmax reads after S, so after this arrival.  Slot j % 4 is free: this warp has filled the pairs
+        // of chunk j - 1, which PV(j - 3) had to release.
+        uint32_t m = seen & 0x11111111u;
+        m = (m | (m >> 3)) & 0x03030303u;
+        m = (m | (m >> 6)) & 0x000F000Fu;
+        m = (m | (m >> 12)) & 0xFFu;
+        reinterpret_cast<uint8_t*>(masks + j % kMaskRing)[warp] = static_cast<uint8_t>(m);
+        mbar_arrive(rope_full(rs));
+      }
+      // value dims 128 q .. 128 q + 127 -> pair slot (4 j + q) mod 8
+#pragma unroll
+      for (int q = 0; q < kPairsPerChunk; ++q) {
+        const int n = j * kPairsPerChunk + q;
+        const int slot = n % kPairRing;
+        ok = mbar_wait(pair_empty(slot), static_cast<uint32_t>((n / kPairRing) & 1) ^ 1u, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_shared16(dst0 + slot * kPairBytes + col[i], tile[q][i]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(pair_full(slot));
@@ -390,30 +390,58 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_lat = idesc_f16_f32(kHeads, kChunk, false, false);
-      constexpr uint32_t idesc_rope = idesc_bf16_f32(kHeads, kChunk, false, false);
-      bool ok = mbar_wait(q_full, 0, abort_flag);
-      // Non-blocking issue of QK^T(qk_j), piece by piece: part 0 is the rope
-      // box (once the S buffer and the rope slot are ready), parts 1-4 one
-      // value pair each.
-      int qk_j = 0, qk_part = 0;
-      long long idle_since = clock64();
-      while (ok && qk_j < nchunks) {
-        bool did = false;
+    constexpr uint32_t idesc_lat = idesc_f16_f32(kHeads, kChunk, false, false);
+    constexpr uint32_t idesc_rope = idesc_bf16_f32(kHeads, kChunk, false, false);
+    constexpr uint32_t idesc_pv = idesc_f16_f32(128, kHeads, true, false);
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const uint32_t acc = __shfl_sync(kAll, tmem, 0);
+    bool ok = __all_sync(kAll, mbar_wait(q_full, 0, abort_flag));
+    // Shared-memory descriptors differ in their low words only, by the address over 16 (see sdesc_sw128).
+    const auto desc_lo = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
+    const auto desc = [](uint32_t lo) { return (sdesc_sw128(0, 0, 1024) & 0xFFFFFFFF00000000ull) | lo; };
+    const uint32_t q_lo = desc_lo(q_s, 16), pair_lo = desc_lo(pairs, 16), rope_lo = desc_lo(rope, 16),
+                   p_lo = desc_lo(p_s, 16), v_lo = desc_lo(pairs, kBoxBytes);
+    // Non-blocking issue: PV(pv_j) as soon as its P is written, otherwise the next piece of QK^T(qk_j): part 0
+    // is the rope box (once the S buffer and the rope slot are ready), parts 1-4 one value pair each.
+    int qk_j = 0, qk_part = 0, pv_j = 0;
+    long long idle_since = clock64();
+    while (ok && pv_j < nchunks) {
+      bool did = false;
+      if (pv_j < qk_j && __all_sync(kAll, mbar_test_wait(p_full, static_cast<uint32_t>(pv_j & 1)))) {
+        // O^T[dims 128 q ..][heads] += V^T P^T, one accumulator block per value pair
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int q = 0; q < kPairsPerChunk; ++q) {
+            const int slot = (pv_j * kPairsPerChunk + q) % kPairRing;
+            const uint32_t v = v_lo + slot * (kPairBytes >> 4);
+            const uint32_t d = acc + q * kHeads;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // A = V^T: M = 128 dims over the pair's two boxes, K = rows 16 kk ..
+              mma_bf16(d, desc(v + kk * (2048 >> 4)), desc(p_lo + kk * 2), idesc_pv, (pv_j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(pair_empty(slot));
+          }
+          mma_commit(p_free);
+        }
+        __syncwarp();
+        ++pv_j;
+        did = true;
+      } else if (qk_j < nchunks) {
         const int sb = qk_j & 1;
-        const uint32_t d = tmem + kSCol + sb * kChunk;
+        const uint32_t d = acc + kSCol + sb * kChunk;
         if (qk_part == 0) {
           const int rs = qk_j % kRopeRing;
-          if (mbar_test_wait(s_free(sb), static_cast<uint32_t>((qk_j >> 1) & 1) ^ 1u) &&
-              mbar_test_wait(rope_full(rs), static_cast<uint32_t>((qk_j / kRopeRing) & 1))) {
+          if (__all_sync(kAll, mbar_test_wait(s_free(sb), static_cast<uint32_t>((qk_j >> 1) & 1) ^ 1u) &&
+                                   mbar_test_wait(rope_full(rs), static_cast<uint32_t>((qk_j / kRopeRing) & 1)))) {
             tc_fence_after();
-            const uint32_t src = rope + rs * kBoxBytes;
+            if (elect_one()) {
+              const uint32_t src = rope_lo + rs * (kBoxBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16(d, sdesc_sw128(q_s + 8 * kQBox + kk * 32, 16, 1024), sdesc_sw128(src + kk * 32, 16, 1024),
-                       idesc_rope, kk > 0 ? 1u : 0u);
-            mma_commit(rope_empty(rs));  // rope dims are not needed for P V
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16(d, desc(q_lo + 8 * (kQBox >> 4) + kk * 2), desc(src + kk * 2), idesc_rope, kk > 0 ? 1u : 0u);
+              mma_commit(rope_empty(rs));  // rope dims are not needed for P V
+            }
+            __syncwarp();
             qk_part = 1;
             did = true;
           }
@@ -421,40 +449,39 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
           const int q = qk_part - 1;
           const int n = qk_j * kPairsPerChunk + q;
           const int slot = n % kPairRing;
-          if (mbar_test_wait(pair_full(slot), static_cast<uint32_t>((n / kPairRing) & 1))) {
+          if (__all_sync(kAll, mbar_test_wait(pair_full(slot), static_cast<uint32_t>((n / kPairRing) & 1)))) {
             tc_fence_after();
-            const uint32_t base = pairs + slot * kPairBytes;
+            const bool last = qk_part == kPairsPerChunk;
+            if (elect_one()) {
+              const uint32_t src = pair_lo + slot * (kPairBytes >> 4);
+              const uint32_t qa = q_lo + 2 * q * (kQBox >> 4);
 #pragma unroll
-            for (int bx = 0; bx < 2; ++bx) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16(d, sdesc_sw128(q_s + (2 * q + bx) * kQBox + kk * 32, 16, 1024),
-                         sdesc_sw128(base + bx * kBoxBytes + kk * 32, 16, 1024), idesc_lat, 1u);
+              for (int kk = 0; kk < 8; ++kk)  // four steps in each of the pair's boxes
+                mma_bf16(d, desc(qa + (kk >> 2) * (kQBox >> 4) + (kk & 3) * 2),
+                         desc(src + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2), idesc_lat, 1u);
+              if (last) mma_commit(s_full(sb));
             }
-            if (qk_part == kPairsPerChunk) {
-              mma_commit(s_full(sb));
-              ++qk_j;
-              qk_part = 0;
-            } else {
-              ++qk_part;
-            }
+            __syncwarp();
+            qk_j += last ? 1 : 0;
+            qk_part = last ? 0 : qk_part + 1;
             did = true;
           }
         }
-        if (did) {
-          idle_since = clock64();
-        } else if (*abort_flag || clock64() - idle_since > kWaitBudgetCycles) {
-          ok = false;
-        }
       }
-      if (!ok) {
-        record_status(p.status, kStatusTimeout);
-        *abort_flag = 1;
+      if (did) {
+        idle_since = clock64();
+      } else if (__any_sync(kAll, *abort_flag || clock64() - idle_since > kWaitBudgetCycles)) {
+        ok = false;
       }
-      mma_commit(qk_done);
-      volatile int never = 0;
-      mbar_wait(qk_done, 0, &never);  // every MMA this thread issued has finished
     }
+    if (!ok && lane == 0) {
+      record_status(p.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    if (elect_one()) mma_commit(o_full);
+    __syncwarp();
+    volatile int never = 0;
+    mbar_wait(o_full, 0, &never);  // every MMA has finished before TMEM is read or freed
   } else {
     // ------------------------------------------------------------ softmax
     // As in sga_attend.cu: thread t of the warp holds rows t/4 and 8 + t/4 of its
@@ -463,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const int m4 = lane & 3;
     const int hrow[2] = {quarter * 16 + (lane >> 2), quarter * 16 + 8 + (lane >> 2)};  // this thread's two heads
+    const uint32_t p_row = p_s + (2 * quarter + ((lane >> 3) & 1)) * 1024 + (lane & 7) * 128;  // stmatrix row
     float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     // Every softmax thread runs every iteration, even after a wait ran out
     // (the abort flag then makes each later wait return at once), so the
@@ -476,20 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       float r[32];
       tmem_ld_16x256b_x8(tmem + lane_addr + kSCol + sb * kChunk, r);
       tc_fence_before();
-      mbar_arrive(s_free(sb));
-      const int mb = j % kMaskRing;
-      ok = ok && mbar_wait(mask_full(mb), static_cast<uint32_t>((j / kMaskRing) & 1), abort_flag);
-      const uint64_t mk = *reinterpret_cast<volatile uint64_t*>(masks + mb);
-      mbar_arrive(mask_empty(mb));
-      // x[i][2k + e] = score of row i at column 8k + 2 m4 + e (masked slots -> -inf)
-      float x[2][16];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free(sb));
+      // r[4k + 2i + e] = q.c of row i at column 8k + 2 m4 + e; masked slots -> -inf
+      const uint64_t mk = *reinterpret_cast<volatile uint64_t*>(masks + j % kMaskRing);
+      if (mk != ~0ull) {
+        const uint64_t mine = mk >> (2 * m4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 8; ++k) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool valid = (mk >> (8 * k + 2 * m4 + e)) & 1ull;
-          x[0][2 * k + e] = valid ? r[4 * k + e] * sc[0] : -INFINITY;
-          x[1][2 * k + e] = valid ? r[4 * k + 2 + e] * sc[1] : -INFINITY;
+          for (int e = 0; e < 2; ++e) {
+            if (!((mine >> (8 * k + e)) & 1ull)) r[4 * k + e] = r[4 * k + 2 + e] = -INFINITY;
+          }
         }
       }
       float alpha[2];
@@ -499,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         float mp[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          mp[c] = fmaxf(fmaxf(x[i][4 * c], x[i][4 * c + 1]), fmaxf(x[i][4 * c + 2], x[i][4 * c + 3]));
+          mp[c] = fmaxf(fmaxf(r[8 * c + 2 * i], r[8 * c + 2 * i + 1]), fmaxf(r[8 * c + 4 + 2 * i], r[8 * c + 5 + 2 * i]));
         float mt = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
         mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
-        mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2));
+        mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2)) * sc[i];  // the scale is positive
         alpha[i] = 1.f;
         if (m_ref[i] == -INFINITY) {
           m_ref[i] = mt;  // nothing accumulated yet (all earlier weights were zero)
@@ -511,16 +537,17 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
           m_ref[i] = mt;
           resc = true;
         }
+        // weights of the row, in place of its scores; every slot so far empty: -inf - 0, all weights zero
+        const float m_p = m_ref[i] == -INFINITY ? 0.f : m_ref[i] - kPShift;
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
-        if (m_ref[i] == -INFINITY) {  // every slot so far is empty: all weights are zero
 #pragma unroll
-          for (int c = 0; c < 16; ++c) x[i][c] = 0.f;
-        } else {
-          const float m_p = m_ref[i] - kPShift;
+        for (int k = 0; k < 8; ++k) {
+          // scaled first and rounded, so that the maximum's difference is exact however large the scores are
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            x[i][c] = fast_exp2(x[i][c] - m_p);
-            ps[c & 3] += x[i][c];
+          for (int e = 0; e < 2; ++e) {
+            const float x = fast_exp2(__fsub_rn(__fmul_rn(r[4 * k + 2 * i + e], sc[i]), m_p));
+            r[4 * k + 2 * i + e] = x;
+            ps[2 * (k & 1) + e] += x;
           }
         }
         float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
@@ -548,45 +575,23 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         }
         named_barrier(1, kSoftmaxThreads);
       }
-      // P[head][row] in the 128-byte-swizzled K-major layout (8 heads per 1 KB
-      // atom); this thread writes the fp16 pairs of columns 8k + 2 m4, +1.
+      // P[head][row] in the 128-byte-swizzled K-major layout (8 heads per 1 KB atom).  A thread's values are two
+      // columns of row t/4 of 8 x 8 blocks, the layout stmatrix takes: four blocks (two of heads, two of columns)
+      // at a time, the row addresses from lanes 8 b .. 8 b + 7 for block b.
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = hrow[i];
-        const uint32_t rbase = (h >> 3) * 1024 + (h & 7) * 128 + 4 * m4;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint32_t*>(p_ptr + rbase + ((k ^ (h & 7)) << 4)) = pack_f16(x[i][2 * k], x[i][2 * k + 1]);
-      }
+      for (int k = 0; k < 8; k += 2)
+        stmatrix_x4(p_row + (((k + (lane >> 4)) ^ (lane & 7)) << 4), pack_f16(r[4 * k], r[4 * k + 1]),
+                    pack_f16(r[4 * k + 2], r[4 * k + 3]), pack_f16(r[4 * k + 4], r[4 * k + 5]),
+                    pack_f16(r[4 * k + 6], r[4 * k + 7]));
       fence_proxy_async_smem();
       tc_fence_before();
-      named_barrier(2, kSoftmaxThreads);  // P_j (and any rescale of O) complete
-      if (threadIdx.x == kPvThread) {
-        // PV(j): O^T[dims 128 q ..][heads] += V_j^T P^T, one accumulator block per value pair
-        constexpr uint32_t idesc_pv = idesc_f16_f32(128, kHeads, true, false);
-        tc_fence_after();
-        for (int q = 0; q < kPairsPerChunk; ++q) {
-          const int slot = (j * kPairsPerChunk + q) % kPairRing;
-          const uint32_t base = pairs + slot * kPairBytes;
-          const uint32_t d = tmem + q * kHeads;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // A = V^T: M = 128 dims over the pair's two boxes, K = rows 16 kk ..
-            mma_bf16(d, sdesc_sw128(base + kk * 2048, kBoxBytes, 1024), sdesc_sw128(p_s + kk * 32, 16, 1024), idesc_pv,
-                     (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(pair_empty(slot));
-        }
-        mma_commit(p_free);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);  // P_j and any rescale of O
     }
-    if (threadIdx.x == kPvThread) mma_commit(o_full);  // every PV this thread issued
-    const bool have_o = ok && mbar_wait(o_full, 0, abort_flag);
-    if (!have_o) {
+    ok = ok && mbar_wait(o_full, 0, abort_flag);
+    if (!ok) {
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
-      if (threadIdx.x == kPvThread) {  // its MMAs must be done before TMEM is freed
-        volatile int never = 0;
-        mbar_wait(o_full, 0, &never);
-      }
     }
     if (m4 == 0) {
       own_ml[hrow[0]] = make_float2(m_ref[0], l_run[0]);
