@@ -51,14 +51,15 @@ constexpr int kQPieces = kDq / 8;            // 16-byte pieces of a query head
 constexpr int kPBytes = kHeads * kChunk * 2;  // 64 heads x 64 rows fp16
 constexpr int kMaskRing = 4;
 constexpr int kProducerWarps = 8;            // warps 0-7: four threads per chunk row
-constexpr int kMmaWarp = 8;
-constexpr int kSoftmaxThreads = 128;         // warps 9-12
-constexpr int kThreads = 32 * (kMmaWarp + 1) + kSoftmaxThreads;
+constexpr int kQkWarp = 8;                   // issues QK^T; warp 9 issues PV
+constexpr int kSoftmaxWarp = 10;             // warps 10-13
+constexpr int kSoftmaxThreads = 128;
+constexpr int kThreads = 32 * kSoftmaxWarp + kSoftmaxThreads;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;
 // barriers: pair_full[8] pair_empty[8] rope_full[2] rope_empty[2] q_full s_full[2] s_free[2]
-//           p_full p_free o_full
-constexpr int kNumBars = 2 * kPairRing + 2 * kRopeRing + 1 + 2 + 2 + 3;
+//           p_full p_free o_full qk_done
+constexpr int kNumBars = 2 * kPairRing + 2 * kRopeRing + 1 + 2 + 2 + 4;
 constexpr int kMaxSplits = 8;                // splits of a query = CTAs of its cluster
 constexpr size_t kSmemBytes = 1024 + kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes + kPBytes +
                               kNumBars * 8 + kMaskRing * 8 + 2 * kHeads * 4 + kHeads * 8 + 16;
@@ -204,7 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
   auto s_free = [&](int b) { return q_full + 8u * (3 + b); };
   const uint32_t p_full = q_full + 8u * 5;
   const uint32_t p_free = q_full + 8u * 6;
-  const uint32_t o_full = q_full + 8u * 7;  // every MMA has finished
+  const uint32_t o_full = q_full + 8u * 7;   // every PV MMA has finished
+  const uint32_t qk_done = q_full + 8u * 8;  // every QK^T MMA has finished
   uint64_t* masks = bars + kNumBars;
   float* head_f = reinterpret_cast<float*>(masks + kMaskRing);  // [64] per-head factors
   float* q_scale = head_f + kHeads;                              // [64] softmax scale (log2) of the scaled heads
@@ -238,10 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     mbar_init(p_full, kSoftmaxThreads / 32);
     mbar_init(p_free, 1);
     mbar_init(o_full, 1);
+    mbar_init(qk_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -313,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         st_shared16(q_s + (c >> 3) * kQBox + h * 128 + (((c & 7) ^ (h & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
       }
       if (part == 0) q_scale[h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
@@ -355,7 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         cur_valid = load(cur, ahead_idx);
         ahead_idx = load_idx(j + 2);
       }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         // Validity of the warp's eight rows (every fourth ballot bit) -> bits 8 warp .. of the chunk's mask, which
@@ -378,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) st_shared16(dst0 + slot * kPairBytes + col[i], tile[q][i]);
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(pair_full(slot));
       }
@@ -388,100 +388,91 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_lat = idesc_f16_f32(kHeads, kChunk, false, false);
-    constexpr uint32_t idesc_rope = idesc_bf16_f32(kHeads, kChunk, false, false);
-    constexpr uint32_t idesc_pv = idesc_f16_f32(128, kHeads, true, false);
+  } else if (warp < kSoftmaxWarp) {
+    // ------------------------------------------------------------ MMA issuers
+    // One warp issues QK^T and one PV, each waiting on its own operands only.  The tiles, Q and P come from ordinary
+    // stores: they are made visible to the tensor core here, between the wait for them and the MMA (the same fence in
+    // the storing warps would also wait for the rows they have in flight).  Shared-memory descriptors differ in
+    // their low words only, by the address over 16 (see sdesc_sw128).
     constexpr uint32_t kAll = 0xFFFFFFFFu;
     const uint32_t acc = __shfl_sync(kAll, tmem, 0);
-    bool ok = __all_sync(kAll, mbar_wait(q_full, 0, abort_flag));
-    // Shared-memory descriptors differ in their low words only, by the address over 16 (see sdesc_sw128).
     const auto desc_lo = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
     const auto desc = [](uint32_t lo) { return (sdesc_sw128(0, 0, 1024) & 0xFFFFFFFF00000000ull) | lo; };
-    const uint32_t q_lo = desc_lo(q_s, 16), pair_lo = desc_lo(pairs, 16), rope_lo = desc_lo(rope, 16),
-                   p_lo = desc_lo(p_s, 16), v_lo = desc_lo(pairs, kBoxBytes);
-    // Non-blocking issue: PV(pv_j) as soon as its P is written, otherwise the next piece of QK^T(qk_j): part 0
-    // is the rope box (once the S buffer and the rope slot are ready), parts 1-4 one value pair each.
-    int qk_j = 0, qk_part = 0, pv_j = 0;
-    long long idle_since = clock64();
-    while (ok && pv_j < nchunks) {
-      bool did = false;
-      if (pv_j < qk_j && __all_sync(kAll, mbar_test_wait(p_full, static_cast<uint32_t>(pv_j & 1)))) {
-        // O^T[dims 128 q ..][heads] += V^T P^T, one accumulator block per value pair
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int q = 0; q < kPairsPerChunk; ++q) {
-            const int slot = (pv_j * kPairsPerChunk + q) % kPairRing;
-            const uint32_t v = v_lo + slot * (kPairBytes >> 4);
-            const uint32_t d = acc + q * kHeads;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // A = V^T: M = 128 dims over the pair's two boxes, K = rows 16 kk ..
-              mma_bf16(d, desc(v + kk * (2048 >> 4)), desc(p_lo + kk * 2), idesc_pv, (pv_j > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(pair_empty(slot));
-          }
-          mma_commit(p_free);
-        }
-        __syncwarp();
-        ++pv_j;
-        did = true;
-      } else if (qk_j < nchunks) {
-        const int sb = qk_j & 1;
+    bool ok = true;
+    if (warp == kQkWarp) {
+      constexpr uint32_t idesc_lat = idesc_f16_f32(kHeads, kChunk, false, false);
+      constexpr uint32_t idesc_rope = idesc_bf16_f32(kHeads, kChunk, false, false);
+      const uint32_t q_lo = desc_lo(q_s, 16), pair_lo = desc_lo(pairs, 16), rope_lo = desc_lo(rope, 16);
+      ok = __all_sync(kAll, mbar_wait(q_full, 0, abort_flag));
+      for (int j = 0; j < nchunks && ok; ++j) {
+        const int sb = j & 1, rs = j % kRopeRing;
         const uint32_t d = acc + kSCol + sb * kChunk;
-        if (qk_part == 0) {
-          const int rs = qk_j % kRopeRing;
-          if (__all_sync(kAll, mbar_test_wait(s_free(sb), static_cast<uint32_t>((qk_j >> 1) & 1) ^ 1u) &&
-                                   mbar_test_wait(rope_full(rs), static_cast<uint32_t>((qk_j / kRopeRing) & 1)))) {
-            tc_fence_after();
-            if (elect_one()) {
+        ok = mbar_wait(s_free(sb), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag) &&
+             mbar_wait(rope_full(rs), static_cast<uint32_t>((j / kRopeRing) & 1), abort_flag);
+        // the rope box and two pairs, then the other two: few waits, and the second half overlaps its pairs' stores
+        for (int half = 0; half < 2 && ok; ++half) {
+          const int n = j * kPairsPerChunk + 2 * half;
+          const int slot = n % kPairRing;
+          const uint32_t ph = static_cast<uint32_t>((n / kPairRing) & 1);
+          ok = __all_sync(kAll, ok && mbar_wait(pair_full(slot), ph, abort_flag) &&
+                                    mbar_wait(pair_full(slot + 1), ph, abort_flag));
+          if (!ok) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          if (elect_one()) {
+            if (half == 0) {
               const uint32_t src = rope_lo + rs * (kBoxBytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 mma_bf16(d, desc(q_lo + 8 * (kQBox >> 4) + kk * 2), desc(src + kk * 2), idesc_rope, kk > 0 ? 1u : 0u);
               mma_commit(rope_empty(rs));  // rope dims are not needed for P V
             }
-            __syncwarp();
-            qk_part = 1;
-            did = true;
-          }
-        } else {
-          const int q = qk_part - 1;
-          const int n = qk_j * kPairsPerChunk + q;
-          const int slot = n % kPairRing;
-          if (__all_sync(kAll, mbar_test_wait(pair_full(slot), static_cast<uint32_t>((n / kPairRing) & 1)))) {
-            tc_fence_after();
-            const bool last = qk_part == kPairsPerChunk;
-            if (elect_one()) {
-              const uint32_t src = pair_lo + slot * (kPairBytes >> 4);
-              const uint32_t qa = q_lo + 2 * q * (kQBox >> 4);
+            const uint32_t src = pair_lo + slot * (kPairBytes >> 4);
+            const uint32_t qa = q_lo + 4 * half * (kQBox >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)  // four steps in each of the pair's boxes
-                mma_bf16(d, desc(qa + (kk >> 2) * (kQBox >> 4) + (kk & 3) * 2),
-                         desc(src + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2), idesc_lat, 1u);
-              if (last) mma_commit(s_full(sb));
-            }
-            __syncwarp();
-            qk_j += last ? 1 : 0;
-            qk_part = last ? 0 : qk_part + 1;
-            did = true;
+            for (int kk = 0; kk < 16; ++kk)  // four steps in each of the two pairs' boxes
+              mma_bf16(d, desc(qa + (kk >> 2) * (kQBox >> 4) + (kk & 3) * 2),
+                       desc(src + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2), idesc_lat, 1u);
+            if (half == 1) mma_commit(s_full(sb));
           }
+          __syncwarp();
         }
+        ok = __all_sync(kAll, ok);
       }
-      if (did) {
-        idle_since = clock64();
-      } else if (__any_sync(kAll, *abort_flag || clock64() - idle_since > kWaitBudgetCycles)) {
-        ok = false;
+    } else {
+      constexpr uint32_t idesc_pv = idesc_f16_f32(128, kHeads, true, false);
+      const uint32_t p_lo = desc_lo(p_s, 16), v_lo = desc_lo(pairs, kBoxBytes);
+      for (int j = 0; j < nchunks; ++j) {
+        ok = __all_sync(kAll, mbar_wait(p_full, static_cast<uint32_t>(j & 1), abort_flag));
+        if (!ok) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        if (elect_one()) {
+          // O^T[dims 128 q ..][heads] += V^T P^T, one accumulator block per value pair
+#pragma unroll
+          for (int q = 0; q < kPairsPerChunk; ++q) {
+            const int slot = (j * kPairsPerChunk + q) % kPairRing;
+            const uint32_t v = v_lo + slot * (kPairBytes >> 4);
+            const uint32_t d = acc + q * kHeads;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // A = V^T: M = 128 dims over the pair's two boxes, K = rows 16 kk ..
+              mma_bf16(d, desc(v + kk * (2048 >> 4)), desc(p_lo + kk * 2), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(pair_empty(slot));
+          }
+          mma_commit(p_free);
+        }
+        __syncwarp();
       }
     }
     if (!ok && lane == 0) {
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
     }
-    if (elect_one()) mma_commit(o_full);
+    const uint32_t done = warp == kQkWarp ? qk_done : o_full;
+    if (elect_one()) mma_commit(done);
     __syncwarp();
     volatile int never = 0;
-    mbar_wait(o_full, 0, &never);  // every MMA has finished before TMEM is read or freed
+    mbar_wait(done, 0, &never);  // this warp's MMAs have finished before TMEM is read or freed
   } else {
     // ------------------------------------------------------------ softmax
     // As in sga_attend.cu: thread t of the warp holds rows t/4 and 8 + t/4 of its
@@ -583,7 +574,6 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         stmatrix_x4(p_row + (((k + (lane >> 4)) ^ (lane & 7)) << 4), pack_f16(r[4 * k], r[4 * k + 1]),
                     pack_f16(r[4 * k + 2], r[4 * k + 3]), pack_f16(r[4 * k + 4], r[4 * k + 5]),
                     pack_f16(r[4 * k + 6], r[4 * k + 7]));
-      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);  // P_j and any rescale of O
@@ -609,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
   } else {
     __syncthreads();
   }
-  if (warp > kMmaWarp && lane < 16) {
+  if (warp >= kSoftmaxWarp && lane < 16) {
     const int head = (warp & 3) * 16 + lane;
     const float g = p.gate ? sigmoidf_(bf16_bits_to_float(p.gate[static_cast<size_t>(row) * kHeads + head])) : 1.f;
     float f;
@@ -640,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
   // those dims into the owner's receive buffer [source split][head][kStride].
   const int kStride = 4 * ((kDv / 4 + S - 1) / S);  // floats per (source, head) row: the widest slice
   float* recv = o_stage;
-  if (warp != kMmaWarp) {
+  if (warp < kProducerWarps || warp >= kSoftmaxWarp) {
     // Twelve warps read O^T out of TMEM: warp w reads lane quarter w % 4; the
     // producer warps 0-3 take dim block 0, 4-7 block 1, the softmax warps blocks 2-3.
     // O^T block b: this lane holds dim 128 b + 32 quarter + lane for all 64 heads.
@@ -695,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
