@@ -108,7 +108,10 @@ struct StreamCfg {
 
 struct StreamParams {
   int n, m, n_blocks, k_blocks, units;  // units: pairs of K blocks in a tile
-  long long total;                      // units of all tiles
+  int total;                            // units of all tiles
+  // Thread block c's range of units.  splits > 0: the (c % splits)-th of `splits` parts of tile c / splits; else one
+  // of gridDim.x equal ranges over all tiles, `base` units and one more for the first `more` of them.
+  int splits, base, more;
   const float* x_scale;
   const float* w_scale;
   float* out_f32;
@@ -120,19 +123,26 @@ struct StreamParams {
 
 // One thread block's part of one tile: units [u0, u1) of `units`.
 struct Segment {
-  int mt, nb, u0, u1;
-  long long tile;
+  int tile, mt, nb, u0, u1;
 };
 
-__device__ __forceinline__ long long range_begin(const StreamParams& p, int c) { return p.total * c / gridDim.x; }
+__device__ __forceinline__ int range_begin(const StreamParams& p, int c) {
+  if (p.splits > 0) return c / p.splits * p.units + p.units * (c % p.splits) / p.splits;
+  return c * p.base + min(c, p.more);
+}
+// The thread block whose range holds unit x.
+__device__ __forceinline__ int range_of(const StreamParams& p, int x) {
+  const int cut = p.more * (p.base + 1);
+  return x < cut ? x / (p.base + 1) : p.more + (x - cut) / p.base;
+}
 
-__device__ __forceinline__ Segment segment_at(const StreamParams& p, long long x, long long end) {
+__device__ __forceinline__ Segment segment_at(const StreamParams& p, int x, int end) {
   Segment s;
   s.tile = x / p.units;
-  s.u0 = static_cast<int>(x - s.tile * p.units);
-  s.u1 = static_cast<int>(min(static_cast<long long>(p.units), s.u0 + (end - x)));
-  s.nb = static_cast<int>(s.tile % p.n_blocks);
-  s.mt = static_cast<int>(s.tile / p.n_blocks);
+  s.u0 = x - s.tile * p.units;
+  s.u1 = min(p.units, s.u0 + (end - x));
+  s.mt = s.tile / p.n_blocks;
+  s.nb = s.tile - s.mt * p.n_blocks;
   return s;
 }
 
@@ -157,7 +167,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
+  const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
   grid_launch_dependents();
-  const long long begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
+  const int begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -199,7 +210,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       uint32_t ph = 0;
       long long issued = 0;
       bool ok = true;
-      for (long long x = begin; x < end && ok;) {
+      for (int x = begin; x < end && ok;) {
         const Segment sg = segment_at(p, x, end);
         for (int u = sg.u0; u < sg.u1; ++u) {
           if (!mbar_wait(empty(st), ph ^ 1u, abort_flag)) {
@@ -232,53 +243,54 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, NP);
-      int st = 0, buf = 0;
-      uint32_t ph = 0, aph = 0;
-      bool ok = true;
-      for (long long x = begin; x < end && ok;) {
-        const Segment sg = segment_at(p, x, end);
-        for (int u = sg.u0; u < sg.u1 && ok; ++u) {
-          if (!mbar_wait(full(st), ph, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const int nkb = min(kUnit, p.k_blocks - kUnit * u);
-          const uint32_t a = ring + st * Cfg::kStageBytes;
-          for (int h = 0; h < nkb; ++h) {
-            if (!mbar_wait(accempty(buf), aph ^ 1u, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    constexpr uint32_t idesc = idesc_e4m3_f32(kTileM, NP);
+    const uint32_t acc = __shfl_sync(kAll, tmem, 0);
+    int st = 0, buf = 0;
+    uint32_t ph = 0, aph = 0;
+    bool ok = true;
+    for (int x = begin; x < end && ok;) {
+      const Segment sg = segment_at(p, x, end);
+      for (int u = sg.u0; u < sg.u1 && ok; ++u) {
+        ok = __all_sync(kAll, mbar_wait(full(st), ph, abort_flag));
+        if (!ok) break;
+        const int nkb = min(kUnit, p.k_blocks - kUnit * u);
+        const uint32_t a = ring + st * Cfg::kStageBytes;
+        for (int h = 0; h < nkb; ++h) {
+          ok = __all_sync(kAll, mbar_wait(accempty(buf), aph ^ 1u, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 K elements (bytes) per MMA
-              mma_e4m3(tmem + buf * NP, sdesc_sw128(a + h * kWBytes + kk * 32, 16, 1024),
+              mma_e4m3(acc + buf * NP, sdesc_sw128(a + h * kWBytes + kk * 32, 16, 1024),
                        sdesc_sw128(a + kUnit * kWBytes + h * Cfg::kXBytes + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
             mma_commit(accfull(buf));
-            if (++buf == kAccBufs) {
-              buf = 0;
-              aph ^= 1u;
-            }
           }
-          if (!ok) break;
-          mma_commit(empty(st));
-          if (++st == Cfg::kStages) {
-            st = 0;
-            ph ^= 1u;
+          __syncwarp();
+          if (++buf == kAccBufs) {
+            buf = 0;
+            aph ^= 1u;
           }
         }
-        x += sg.u1 - sg.u0;
+        if (!ok) break;
+        if (elect_one()) mma_commit(empty(st));
+        __syncwarp();
+        if (++st == Cfg::kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
-      if (!ok) {
-        record_status(p.status, kStatusTimeout);
-        *abort_flag = 1;
-      }
-      mma_commit(done_bar);
-      volatile int never = 0;
-      mbar_wait(done_bar, 0, &never);  // every MMA has finished before TMEM is freed
+      x += sg.u1 - sg.u0;
     }
+    if (!ok && lane == 0) {
+      record_status(p.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    if (elect_one()) mma_commit(done_bar);
+    __syncwarp();
+    volatile int never = 0;
+    mbar_wait(done_bar, 0, &never);  // every MMA has finished before TMEM is freed
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales
     // Products x_scale * w_scale of up to 16 K blocks at a time, two slots.
@@ -286,7 +298,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int slot = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (long long x = begin; x < end && ok;) {
+    for (int x = begin; x < end && ok;) {
       const Segment sg = segment_at(p, x, end);
       const float* ws = p.w_scale + static_cast<size_t>(sg.mt) * p.k_blocks;
       for (int kb0 = kUnit * sg.u0; kb0 < kUnit * sg.u1; kb0 += kChunk) {
@@ -295,15 +307,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           break;
         }
         float* dst = scales + slot * kChunk * NP;
-#pragma unroll 8
-        for (int i = t; i < kChunk * NP; i += 64) {
-          const int kbl = i % kChunk, tok = i / kChunk, kb = kb0 + kbl;
-          const int token = sg.nb * NP + tok;
-          float v = 0.f;
-          if (kb < p.k_blocks && token < p.n)
-            v = __ldg(p.x_scale + static_cast<size_t>(token) * p.k_blocks + kb) * __ldg(ws + kb);
-          dst[kbl * NP + tok] = v;
-        }
+        // this thread's K block and every fourth token, all loads before the first store (addresses past the end are
+        // clamped: their products scale zeros or go unused)
+        const int kbl = t % kChunk, tok0 = t / kChunk, kb = min(kb0 + kbl, p.k_blocks - 1);
+        const float wv = __ldg(ws + kb);
+        float v[NP / 4];
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i)
+          v[i] = __ldg(p.x_scale + static_cast<size_t>(min(sg.nb * NP + tok0 + 4 * i, p.n - 1)) * p.k_blocks + kb);
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i) dst[kbl * NP + tok0 + 4 * i] = v[i] * wv;
         mbar_arrive(sfull(slot));
         slot ^= 1;
         if (slot == 0) ph ^= 1u;
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int buf = 0, slot = 0;
     uint32_t aph = 0, sph = 0;
     bool ok = true;
-    for (long long x = begin; x < end && ok;) {
+    for (int x = begin; x < end && ok;) {
       const Segment sg = segment_at(p, x, end);
       x += sg.u1 - sg.u0;
       float acc[NP];
@@ -377,9 +390,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       bool write = true;
       if (sg.u0 != 0 || sg.u1 != p.units) {
         // A shared tile: leave the partial sums, and let the last of the tile's ranges add them all in order.
-        const long long t0 = sg.tile * p.units;
-        const int c0 = static_cast<int>(((t0 + 1) * gridDim.x - 1) / p.total);            // range of its first unit
-        const int c1 = static_cast<int>(((t0 + p.units) * gridDim.x - 1) / p.total);      // and of its last
+        const int t0 = sg.tile * p.units;
+        const int c0 = p.splits > 0 ? sg.tile * p.splits : range_of(p, t0);  // the tile's first range, and its last
+        const int c1 = p.splits > 0 ? c0 + p.splits - 1 : range_of(p, t0 + p.units - 1);
         auto part_of = [&](int c) {
           const int second = range_begin(p, c) / p.units != sg.tile;  // a range's first tile, or its last
           return p.part + (static_cast<size_t>(2 * c + second) * NP) * kTileM + mrow;
@@ -387,9 +400,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         float* mine = part_of(blockIdx.x);
 #pragma unroll
         for (int i = 0; i < NP; ++i) mine[i * kTileM] = acc[i];
-        __threadfence();
         named_barrier(1, 128);
         if (threadIdx.x == 128) {
+          __threadfence();  // after the barrier: covers every thread's partial sums
           const int before = atomicAdd(p.counters + c0, 1);
           *last_flag = before == c1 - c0;
           if (before == c1 - c0) p.counters[c0] = 0;
@@ -400,10 +413,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (write) {
 #pragma unroll
           for (int i = 0; i < NP; ++i) acc[i] = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* from = part_of(c);
+          // 128 loads a thread in flight (several ranges at a time for few tokens), added in range order
+          constexpr int kAtOnce = 128 / NP;
+          for (int c = c0; c <= c1; c += kAtOnce) {
+            float v[kAtOnce][NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) acc[i] += __ldcg(from + i * kTileM);
+            for (int q = 0; q < kAtOnce; ++q) {
+              const float* from = part_of(min(c + q, c1));
+#pragma unroll
+              for (int i = 0; i < NP; ++i) v[q][i] = __ldcg(from + i * kTileM);
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+              if (c + q > c1) break;
+#pragma unroll
+              for (int i = 0; i < NP; ++i) acc[i] += v[q][i];
+            }
           }
         }
         named_barrier(1, 128);  // last_flag read by all before the next tile writes it
@@ -447,7 +472,30 @@ cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   p.n_blocks = (a.n + NP - 1) / NP;
   p.k_blocks = (a.k + kBlock - 1) / kBlock;
   p.units = (p.k_blocks + kUnit - 1) / kUnit;
-  p.total = static_cast<long long>((a.m + kTileM - 1) / kTileM) * p.n_blocks * p.units;
+  const long long tiles = static_cast<long long>((a.m + kTileM - 1) / kTileM) * p.n_blocks;
+  if (tiles * p.units > INT32_MAX / 2) return cudaErrorInvalidValue;  // over 17 TB of weights
+  p.total = static_cast<int>(tiles) * p.units;
+  const int max_grid = std::min(num_sms, kMaxGrid);
+  int grid = std::min(max_grid, p.total);
+  // Few tiles: every range is a part of one tile (a range over two tiles leaves two partial sums, the first of them
+  // in the middle of its work).  More parts shorten the K loop (~0.55 us a unit) and lengthen the sum that the last
+  // one to arrive takes over all of them (~12 ns a part and token): the number of parts balances the two.
+  p.splits = 0;
+  if (tiles * 2 <= max_grid) {
+    const int most = std::min(max_grid / static_cast<int>(tiles), p.units);
+    float best = 0.f;
+    for (int parts = 1; parts <= most; ++parts) {
+      const float us = 0.55f * static_cast<float>((p.units + parts - 1) / parts) +
+                       (parts > 1 ? 1.5f + 0.012f * static_cast<float>(parts * NP) : 0.f);
+      if (parts == 1 || us < best) {
+        best = us;
+        p.splits = parts;
+      }
+    }
+    grid = static_cast<int>(tiles) * p.splits;
+  }
+  p.base = p.total / grid;
+  p.more = p.total % grid;
   p.x_scale = a.x_scale;
   p.w_scale = a.w_scale;
   p.out_f32 = a.out_f32;
@@ -463,9 +511,377 @@ cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   e = cudaFuncSetAttribute(gemm_fp8_stream_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(Cfg::kSmem));
   if (e != cudaSuccess) return e;
-  const long long grid = std::min<long long>(std::min(num_sms, kMaxGrid), p.total);
   return host::launch_pdl(gemm_fp8_stream_kernel<NP>, dim3(static_cast<unsigned>(grid)), dim3(kStreamThreads),
                           Cfg::kSmem, s, wmap, xmap, p);
+}
+
+// ---------------------------------------------------------------- tiled product (many tokens)
+constexpr int kTM = 128;                       // tokens per CTA: half of MMA M, one token per TMEM lane
+constexpr int kTN = 256;                       // output channels per tile: MMA N, two weight scale blocks
+constexpr int kTStages = 4;                    // even: the two MMA warps take every other stage
+constexpr int kTXBytes = kTM * kBlock;         // one K block of this CTA's tokens: 16 KB
+constexpr int kTWBytes = kTN / 2 * kBlock;     // one K block of this CTA's half of the weights: 16 KB
+constexpr int kTStageBytes = kTXBytes + kTWBytes;
+constexpr int kTChunk = 8;                     // K blocks per scale slot
+constexpr int kTScaleLd = kTM + 1;             // odd: the transposing stores of the scales hit distinct banks
+constexpr int kTScaleFloats = kTChunk * kTScaleLd + 2 * kTChunk;
+constexpr int kTThreads = 384;                 // warps: TMA, MMA (even K blocks, odd ones), scales, 8 of accumulation
+constexpr int kTNumBars = 2 * kTStages + 4 + 4 + 2;
+constexpr int kTOutFloats = 32 * 33;           // one accumulating warp's 32 x 32 transpose for the output
+constexpr size_t kTSmem =
+    1024 + kTStages * kTStageBytes + (2 * kTScaleFloats + 8 * kTOutFloats) * 4 + kTNumBars * 8 + 16;
+static_assert(kTSmem <= 232448, "shared memory budget");
+// Registers at launch: 384 threads x 168 = 64,512, shared out as 128 x 56 + 256 x 224.
+constexpr int kTRegsSmall = 56, kTRegsLarge = 224;
+static_assert(128 * kTRegsSmall + 256 * kTRegsLarge <= 384 * 168, "register split");
+
+struct TileParams {
+  int n, m, n_tiles, m_tiles, k_blocks, tiles;
+  const float* x_scale;
+  const float* w_scale;
+  float* out_f32;
+  uint16_t* out_bf16;
+  int* status;
+};
+
+// (a, b) += (x, y) * s, two lanes an instruction.
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float s) {
+  asm("{\n\t.reg .b64 c, v, t;\n\t"
+      "mov.b64 c, {%0, %1};\n\t"
+      "mov.b64 v, {%2, %3};\n\t"
+      "mov.b64 t, {%4, %4};\n\t"
+      "fma.rn.f32x2 c, v, t, c;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y), "f"(s));
+}
+
+__global__ void __launch_bounds__(kTThreads, 1)
+    gemm_fp8_tile_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                         TileParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(smem);
+  float* scales = reinterpret_cast<float*>(smem + kTStages * kTStageBytes);
+  float* out_stage = scales + 2 * kTScaleFloats;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out_stage + 8 * kTOutFloats);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kTStages + s); };
+  auto accfull = [&](int a) { return bar0 + 8u * (2 * kTStages + a); };
+  auto accempty = [&](int a) { return bar0 + 8u * (2 * kTStages + 2 + a); };
+  auto sfull = [&](int a) { return bar0 + 8u * (2 * kTStages + 4 + a); };
+  auto sempty = [&](int a) { return bar0 + 8u * (2 * kTStages + 6 + a); };
+  auto done = [&](int a) { return bar0 + 8u * (2 * kTStages + 8 + a); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kTNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(accfull(a), 1);
+      mbar_init(accempty(a), 16);  // one arrival per accumulating warp of both CTAs (the leader's is used)
+      mbar_init(sfull(a), 32);
+      mbar_init(sempty(a), 8);
+      mbar_init(done(a), 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&wmap);
+    prefetch_tmap(&xmap);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // both CTAs' barriers are initialised before either signals the other
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // Tiles go over the pairs with the tokens fastest: the pairs at work share few weight tiles and re-read the
+  // tokens, which the L2 holds.
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsSmall));
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        const uint64_t pol = policy_evict_last();
+        int st = 0;
+        uint32_t ph = 0;
+        long long issued = 0;
+        bool ok = true;
+        for (int t = pair; t < p.tiles && ok; t += pairs) {
+          const int tn = t % p.n_tiles, tm = t / p.n_tiles;
+          for (int kb = 0; kb < p.k_blocks; ++kb) {
+            if (!mbar_wait_idle(empty(st), ph ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            // both CTAs' loads complete on the leader's barrier
+            if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * kTStageBytes);
+            const uint32_t dst = ring + st * kTStageBytes;
+            tma_load_2d_pair(dst, &xmap, full(st) & kPairLeaderMask, kb * kBlock, (2 * tn + rank) * kTM, pol);
+            tma_load_2d_pair(dst + kTXBytes, &wmap, full(st) & kPairLeaderMask, kb * kBlock,
+                             tm * kTN + rank * (kTN / 2), pol);
+            ++issued;
+            if (++st == kTStages) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        // The leader's last arrivals on this CTA's `empty` barriers have landed before the CTA may exit.
+        for (int i = 0; i < kTStages && ok; ++i) {
+          ok = mbar_wait_idle(empty(st), ph ^ 1u, abort_flag);
+          if (++st == kTStages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) {
+          record_status(p.status, kStatusTimeout);
+          *abort_flag = 1;
+          volatile int never = 0;
+          if (rank == 0)  // the peer waits for the leader at the cluster barrier below
+            for (long long i = (issued > kTStages ? issued - kTStages : 0); i < issued; ++i)
+              mbar_wait_idle(full(static_cast<int>(i % kTStages)), static_cast<uint32_t>((i / kTStages) & 1), &never);
+        }
+      }
+    } else if (warp < 3) {
+      // ---------------------------------------------------------- MMA issuers (of the leader, for both CTAs)
+      // Two warps take every other K block of the pair's sequence and one accumulator each: a warp's waits for its
+      // next block run while the other's block is in the tensor core (issuing a block takes nearly as long as
+      // computing it, and the waits ~300 cycles more).
+      if (rank == 0) {
+        constexpr uint32_t kAll = 0xFFFFFFFFu;
+        constexpr uint32_t idesc = idesc_e4m3_f32(2 * kTM, kTN);
+        const int buf = warp - 1;
+        const uint32_t acc = __shfl_sync(kAll, tmem, 0) + buf * kTN;
+        const int my_tiles = (p.tiles - pair + pairs - 1) / pairs;
+        const long long blocks = static_cast<long long>(my_tiles) * p.k_blocks;
+        int st = buf;
+        uint32_t ph = 0, aph = 0;
+        bool ok = true;
+        for (long long i = buf; i < blocks; i += 2) {
+          ok = __all_sync(kAll, mbar_wait_idle(full(st), ph, abort_flag) && mbar_wait_idle(accempty(buf), aph ^ 1u, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t a = ring + st * kTStageBytes;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 32 K elements (bytes) per MMA
+              mma_e4m3_pair(acc, sdesc_sw128(a + kk * 32, 16, 1024), sdesc_sw128(a + kTXBytes + kk * 32, 16, 1024),
+                            idesc, kk > 0 ? 1u : 0u);
+            mma_commit_pair(accfull(buf));
+            mma_commit_pair(empty(st));
+          }
+          __syncwarp();
+          st += 2;  // the ring has an even number of stages
+          if (st >= kTStages) {
+            st -= kTStages;
+            ph ^= 1u;
+          }
+          aph ^= 1u;
+        }
+        if (!ok && lane == 0) {
+          record_status(p.status, kStatusTimeout);
+          *abort_flag = 1;
+        }
+        if (elect_one()) mma_commit_pair_here(done(buf));
+        __syncwarp();
+        volatile int never = 0;
+        mbar_wait_idle(done(buf), 0, &never);  // every MMA has finished before TMEM is freed
+      }
+    } else {
+      // ---------------------------------------------------------- scales
+      // Token scales of up to 8 K blocks at a time, transposed to [K block][token], and the two weight scales.
+      const int m_blocks = (p.m + kBlock - 1) / kBlock;
+      int slot = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = pair; t < p.tiles && ok; t += pairs) {
+        const int tn = t % p.n_tiles, tm = t / p.n_tiles;
+        for (int kb0 = 0; kb0 < p.k_blocks; kb0 += kTChunk) {
+          if (!mbar_wait_idle(sempty(slot), ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          float* dst = scales + slot * kTScaleFloats;
+          // 16 loads before their stores (addresses past the end are clamped, their values dropped)
+          const int kbl = lane % kTChunk, tok0 = lane / kTChunk, kb = kb0 + kbl;
+          const float* col = p.x_scale + min(kb, p.k_blocks - 1);
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            const int tok1 = tok0 + part * (kTM / 2);
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              v[i] = __ldg(col + static_cast<size_t>(min((2 * tn + rank) * kTM + tok1 + 4 * i, p.n - 1)) * p.k_blocks);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dst[kbl * kTScaleLd + tok1 + 4 * i] = v[i];
+          }
+          if (lane < 2 * kTChunk) {
+            const int mb = 2 * tm + lane / kTChunk;
+            dst[kTChunk * kTScaleLd + lane] = kb < p.k_blocks && mb < m_blocks
+                                                  ? __ldg(p.w_scale + static_cast<size_t>(mb) * p.k_blocks + kb)
+                                                  : 0.f;
+          }
+          mbar_arrive(sfull(slot));
+          slot ^= 1;
+          if (slot == 0) ph ^= 1u;
+        }
+      }
+      if (!ok) {
+        record_status(p.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsLarge));
+    // ------------------------------------------------------------ scaled accumulation
+    // Warp w: lane quarter w % 4 (token 32 (w % 4) + lane), the 128 channels of scale block `half`.
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t src0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kBlock;
+    const int tok = quarter * 32 + lane;
+    int buf = 0, slot = 0;
+    uint32_t aph = 0, sph = 0;
+    bool ok = true;
+    for (int t = pair; t < p.tiles && ok; t += pairs) {
+      const int tn = t % p.n_tiles, tm = t / p.n_tiles;
+      float acc[kBlock];
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) acc[i] = 0.f;
+      for (int kb0 = 0; kb0 < p.k_blocks && ok; kb0 += kTChunk) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_idle(sfull(slot), sph, abort_flag));
+        if (!ok) break;
+        const float* sc = scales + slot * kTScaleFloats;
+        const int kbs = min(kTChunk, p.k_blocks - kb0);
+        float s_next = sc[tok] * sc[kTChunk * kTScaleLd + half * kTChunk];
+        for (int kbl = 0; kbl < kbs; ++kbl) {
+          const float s = s_next;
+          if (kbl + 1 < kbs) s_next = sc[(kbl + 1) * kTScaleLd + tok] * sc[kTChunk * kTScaleLd + half * kTChunk + kbl + 1];
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_idle(accfull(buf), aph, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kBlock; c += 32) {
+            float v[32];
+            tmem_ld32(src0 + buf * kTN + c, v);
+            if (c + 32 == kBlock) {  // all of this warp's columns are in registers
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(accempty(buf) & kPairLeaderMask);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], s);
+          }
+          buf ^= 1;
+          if (buf == 0) aph ^= 1u;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty(slot));
+        slot ^= 1;
+        if (slot == 0) sph ^= 1u;
+      }
+      // Output: 32 x 32 pieces turned over in shared memory, so that a store covers 32 consecutive channels of a token
+      // whatever the alignment of its row.
+      const int token0 = (2 * tn + rank) * kTM + quarter * 32, ch0 = tm * kTN + half * kBlock;
+      const int rows = min(32, p.n - token0);
+      if (!ok || rows <= 0) continue;
+      float* stage = out_stage + (warp - 4) * kTOutFloats;
+#pragma unroll
+      for (int c = 0; c < kBlock; c += 32) {
+        if (ch0 + c >= p.m) break;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) stage[lane * 33 + i] = acc[c + i];
+        __syncwarp();
+        const int ch = ch0 + c + lane;
+        if (p.out_bf16 && (p.m & 1) == 0) {  // two tokens a store, two channels a lane
+          const int pair_ch = ch0 + c + 2 * (lane & 15);
+          uint16_t* o = p.out_bf16 + static_cast<size_t>(token0 + (lane >> 4)) * p.m + pair_ch;
+#pragma unroll 8
+          for (int r = 0; r < 32; r += 2, o += 2 * static_cast<size_t>(p.m)) {
+            const float* v = stage + (r + (lane >> 4)) * 33 + 2 * (lane & 15);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
+            if (r + (lane >> 4) < rows && pair_ch < p.m) *reinterpret_cast<__nv_bfloat162*>(o) = b;
+          }
+        } else if (ch < p.m) {
+          const size_t at0 = static_cast<size_t>(token0) * p.m + ch;
+#pragma unroll 8
+          for (int r = 0; r < rows; ++r) {
+            const float v = stage[r * 33 + lane];
+            if (p.out_bf16) {
+              p.out_bf16[at0 + static_cast<size_t>(r) * p.m] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            } else {
+              p.out_f32[at0 + static_cast<size_t>(r) * p.m] = v;
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0) {
+      record_status(p.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // the pair's MMAs, copies and arrivals are done in both CTAs
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+cudaError_t launch_tile(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
+  TileParams p;
+  p.n = a.n;
+  p.m = a.m;
+  p.n_tiles = (a.n + 2 * kTM - 1) / (2 * kTM);
+  p.m_tiles = (a.m + kTN - 1) / kTN;
+  p.k_blocks = (a.k + kBlock - 1) / kBlock;
+  const long long tiles = static_cast<long long>(p.n_tiles) * p.m_tiles;
+  if (tiles > INT32_MAX - num_sms) return cudaErrorInvalidValue;
+  p.tiles = static_cast<int>(tiles);
+  p.x_scale = a.x_scale;
+  p.w_scale = a.w_scale;
+  p.out_f32 = a.out_f32;
+  p.out_bf16 = a.out_bf16;
+  p.status = a.status;
+  CUtensorMap wmap, xmap;
+  cudaError_t e = make_tmap_2d(&wmap, true, a.w, a.k, a.m, a.k, kBlock, kTN / 2);
+  if (e != cudaSuccess) return e;
+  e = make_tmap_2d(&xmap, true, a.x, a.k, a.n, a.k, kBlock, kTM);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gemm_fp8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTSmem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(num_sms / 2, p.tiles)));
+  cfg.blockDim = dim3(kTThreads);
+  cfg.dynamicSmemBytes = kTSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_tile_kernel, wmap, xmap, p);
 }
 
 }  // namespace
@@ -483,7 +899,8 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   if (a.n <= 16) return launch_stream<16>(a, num_sms, s);
   if (a.n <= 32) return launch_stream<32>(a, num_sms, s);
   if (a.n <= 64) return launch_stream<64>(a, num_sms, s);
-  return launch_stream<128>(a, num_sms, s);
+  if (a.n <= 128) return launch_stream<128>(a, num_sms, s);
+  return launch_tile(a, num_sms, s);
 }
 
 }  // namespace sga
