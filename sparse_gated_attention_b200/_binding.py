@@ -155,6 +155,16 @@ def _need(t, name, dtype, shape=None):
     return t
 
 
+def _empty(shape, dtype, device):
+    """A contiguous tensor: torch.empty at half its cost, which counts in a decode step's short calls."""
+    strides, n = [], 1
+    for d in reversed(shape):
+        strides.append(n)
+        n *= d
+    strides.reverse()
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
 def _one_device(*tensors):
     """Every given tensor lives on the current CUDA device: the library launches there, on its streams."""
     dev = torch._C._cuda_getDevice()
@@ -378,7 +388,7 @@ def kv4_read(kv4, pos, kv_rows=None, ws=None, stream=None):
     _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
     _need(pos, "pos", torch.int32, (B, T))
     if kv_rows is None:
-        kv_rows = torch.empty((B, T, QK_DIM), dtype=torch.bfloat16, device=kv4.device)
+        kv_rows = _empty((B, T, QK_DIM), torch.bfloat16, kv4.device)
     else:
         _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
     dims = make_dims(B, T, L)
@@ -401,7 +411,7 @@ def sparse_mla_attend_kv4(q, kv4, idx, gate=None, out=None, ws=None, stream=None
         _need(gate, "gate", torch.bfloat16, (B, T, HEADS))
     dims = make_dims(B, T, L, K)
     if out is None:
-        out = torch.empty((B, T, HEADS, V_DIM), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, HEADS, V_DIM), torch.bfloat16, q.device)
     else:
         _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
     ws = _status_ws(ws, q.device)
@@ -432,7 +442,7 @@ def forward_kv4(q_idx, w, k_idx, q, kv4, gate, q_pos, top_k: int = TOP_K, idx_ou
     if idx_out is not None:
         _need(idx_out, "idx_out", torch.int32, (B, T, top_k))
     if out is None:
-        out = torch.empty((B, T, HEADS, V_DIM), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, HEADS, V_DIM), torch.bfloat16, q.device)
     _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
     if ws is None:
         ws = alloc_workspace(dims, OP_FORWARD, q.device)
@@ -454,11 +464,11 @@ def quantize_fp8(x, codes=None, scale=None, stream=None):
     K = shape[-1]
     s_shape = (*shape[:-1], -(-K // FP8_BLOCK))
     if codes is None:
-        codes = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     else:
         _need_fp8(codes, "codes", shape)
     if scale is None:
-        scale = torch.empty(s_shape, dtype=torch.float32, device=x.device)
+        scale = _empty(s_shape, torch.float32, x.device)
     else:
         _need(scale, "scale", torch.float32, s_shape)
     _one_device(x, codes, scale)
@@ -490,7 +500,7 @@ def gemm_fp8(x, x_scale, w, w_scale, out_dtype=torch.float32, out=None, ws=None,
     if out is None:
         if out_dtype not in _OUT_TYPES:
             raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
-        out = torch.empty((*lead, M), dtype=out_dtype, device=x.device)
+        out = _empty((*lead, M), out_dtype, x.device)
     else:
         out_dtype = out.dtype
         if out_dtype not in _OUT_TYPES:
