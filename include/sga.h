@@ -446,6 +446,55 @@ SGA_API sga_status_t sga_layer_forward(const sga_dims_t* dims, const sga_layer_w
                                        sga_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The layer in few bits: sga_layer_forward with the three large projections
+ * on E4M3 weights (nlp.com.ai "A.X K2 FP8") and the 4-bit latent cache.
+ *   c = quantise(h): sga_quantize_fp8;  [c_q | c_kv, k_rope | k_idx | w] = w_hq c
+ *   kv4[b, q_pos] = [c_kv, rotated k_rope] (sga_kv4_append); k_idx_cache as before
+ *   [q heads | g | q_idx] = w_cq quantise(c_q);  q_lat = W_UK^T q_nope
+ *   idx, out = sga_forward_kv4(...);  o = W_UV out;  y = w_o quantise(o)
+ * with sga_gemm_fp8 for the three products, every activation between two
+ * contractions rounded to bf16 as in sga_layer_forward, and y fp32.
+ *   Weights: E4M3, row-major, one fp32 scale per 128 x 128 block
+ * (scale arrays [ceil(rows / 128)][ceil(columns / 128)]).  Every matrix of a
+ * packed one starts at a multiple of 128 rows, so that a checkpoint's scale
+ * blocks carry over; the rows in between are not used (any finite values):
+ *   w_hq [Rp + 832][D], Rp = R rounded up to 128:  W_DQ from row 0, W_DKV (576)
+ *        from Rp, W_IK (128) from Rp + 640, W_IW (64) from Rp + 768
+ *   w_cq [20608][R]:  W_UQ (12,288) from row 0, W_G (64) from 12,288, W_IQ
+ *        (8,192) from 12,416
+ *   w_o  [D][8192]
+ *   w_uk, w_uv [64][128][512] bf16, as for sga_layer_forward
+ * D = d_model and R = q_rank are multiples of 16.                             */
+typedef struct {
+  int32_t d_model; /* D */
+  int32_t q_rank;  /* R */
+  const sga_fp8_e4m3_t* w_hq;
+  const float* w_hq_scale;
+  const sga_fp8_e4m3_t* w_cq;
+  const float* w_cq_scale;
+  const sga_fp8_e4m3_t* w_o;
+  const float* w_o_scale;
+  const sga_bf16_t* w_uk;
+  const sga_bf16_t* w_uv;
+} sga_layer_fp8_weights_t;
+
+/* Bytes of workspace sga_layer_forward_fp8kv4 needs (256-byte aligned,
+ * zero-filled before the first call; the status word is at its start).
+ * Depends on dims and on weights->d_model / q_rank only. */
+SGA_API sga_status_t sga_layer_fp8kv4_workspace_size(const sga_dims_t* dims, const sga_layer_fp8_weights_t* weights,
+                                                     size_t* bytes);
+
+/* h [B][T][D] bf16, q_pos [B][T] int32, kv4 [B][L][416] bytes, k_idx_cache
+ * [B][L][128] bf16 (both caches: the rows at the new tokens' positions are
+ * overwritten), idx_out [B][T][K] int32 or NULL, y [B][T][D] fp32 (16-byte
+ * aligned).  Device error: a position outside [0, L) (that token's cache rows
+ * are not written). */
+SGA_API sga_status_t sga_layer_forward_fp8kv4(const sga_dims_t* dims, const sga_layer_fp8_weights_t* weights,
+                                              const sga_bf16_t* h, const int32_t* q_pos, uint8_t* kv4,
+                                              sga_bf16_t* k_idx_cache, int32_t* idx_out, float* y, void* ws,
+                                              size_t ws_bytes, sga_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * The indexer's sparse warm-up objective and its gradients (arXiv abstract
  * "A.X K2 Technical Report": the indexer is optimised against its own sparse
  * top-k selection rather than the dense attention distribution; archdb

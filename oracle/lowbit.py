@@ -122,3 +122,51 @@ def attend_kv4(q: np.ndarray, packed: np.ndarray, idx: np.ndarray, gate):
             spread[b, t] = p @ np.abs(rows[:, :LATENT]) * g
             total[b, t] = np.abs(rows[:, :LATENT]).sum(0)
     return out, spread, zabs, total
+
+
+# ----------------------------------------------------------------------------- one layer in few bits
+def _quantised(x: np.ndarray) -> np.ndarray:
+    """The values that quantize_fp8 keeps of x [..., k]."""
+    flat = x.reshape(-1, x.shape[-1])
+    codes, scale = quantize_fp8(flat)
+    return block_scaled(codes, scale, 1).reshape(x.shape)
+
+
+def layer_forward(h, q_pos, packed, k_idx_cache, wts: dict, k: int = 2048, n_threads: int = 0) -> dict:
+    """The layer of sga_layer_forward_fp8kv4 in fp64, every activation between two contractions rounded to bf16.
+
+    packed [B,L,416] bytes and k_idx_cache [B,L,128] are updated copies in the result; wts as layer_forward_fp8kv4
+    takes them.  Dense selections only (all positions 0..q_pos within k), where the indexer plays no part."""
+    from . import layer
+
+    def weights(name):
+        return block_scaled(wts[name].view(torch.uint8).cpu().numpy(), to_f64(wts[name + "_scale"]), 128)
+
+    rb = layer.round_bf16
+    w_hq, w_cq, w_o = weights("w_hq"), weights("w_cq"), weights("w_o")
+    R = w_cq.shape[1]
+    rp = -(-R // BLOCK) * BLOCK
+    H, pos = _quantised(to_f64(h)), q_pos.cpu().numpy().astype(np.int64)
+    B, T = pos.shape
+    g1 = H @ w_hq.T
+    c_q = rb(g1[..., :R])
+    kv_row = np.concatenate([rb(g1[..., rp:rp + LATENT]),
+                             rb(layer.rope(rb(g1[..., rp + LATENT:rp + LATENT + ROPE]), pos))], -1)
+    k_row = rb(g1[..., rp + 640:rp + 768])
+    g2 = _quantised(c_q) @ w_cq.T
+    heads = g2[..., :12288].reshape(B, T, 64, 192)
+    q_rope = rb(layer.rope(rb(heads[..., 128:]), pos[..., None]))
+    q = np.concatenate([rb(np.einsum("bthd,hdj->bthj", rb(heads[..., :128]), to_f64(wts["w_uk"]))), q_rope], -1)
+    gate = rb(g2[..., 12288:12352])
+    packed, k_idx = packed.cpu().numpy().copy(), to_f64(k_idx_cache).copy()
+    code, scale, rope_v = kv4_pack(kv_row.reshape(B * T, -1))
+    bits = layer.bf16_bits(rope_v).view(np.uint8).reshape(B * T, 128)
+    rows = np.concatenate([code[:, 0::2] | (code[:, 1::2] << 4), scale, bits], 1).reshape(B, T, ROW_BYTES)
+    idx = np.full((B, T, k), -1, dtype=np.int32)
+    for b in range(B):
+        for t in range(T):
+            packed[b, pos[b, t]], k_idx[b, pos[b, t]] = rows[b, t], k_row[b, t]
+            idx[b, t, :pos[b, t] + 1] = np.arange(pos[b, t] + 1)
+    out = rb(attend_kv4(q, packed, idx, gate)[0])
+    o = rb(np.einsum("bthj,hij->bthi", out, to_f64(wts["w_uv"]))).reshape(B, T, -1)
+    return {"idx": idx, "packed": packed, "k_idx": k_idx, "y": _quantised(o) @ w_o.T}

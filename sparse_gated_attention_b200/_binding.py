@@ -29,6 +29,7 @@ TOP_K = 2048
 OP_INDEX_SCORES, OP_TOPK_SELECT, OP_SPARSE_MLA_ATTEND, OP_FORWARD, OP_FORWARD_FUSED = 0, 1, 2, 3, 4
 LAYER_PROJECT, LAYER_OUTPUT, LAYER_FORWARD = 0, 1, 2
 # packed layer weights (see sga_layer_weights_t): rows of w_hq after W_DQ, rows of w_cq
+HQ_EXTRA_FP8, CQ_ROWS_FP8 = 832, 20608  # the packed FP8 weights (see sga_layer_fp8_weights_t)
 HQ_EXTRA = QK_DIM + INDEX_DIM + INDEX_HEADS  # 768
 CQ_ROWS = HEADS * 192 + HEADS + INDEX_HEADS * INDEX_DIM  # 20,544
 V_HEAD = 128
@@ -41,7 +42,7 @@ EXPORTED = ["sga_abi_version", "sga_status_string", "sga_workspace_size", "sga_i
             "sga_layer_project", "sga_layer_output", "sga_layer_forward", "sga_indexer_warmup_workspace_size",
             "sga_indexer_warmup", "sga_selftest_bounded_wait", "sga_forward_fused", "sga_forward_fused_fp8",
             "sga_kv4_append", "sga_kv4_read", "sga_sparse_mla_attend_kv4", "sga_forward_kv4", "sga_quantize_fp8",
-            "sga_gemm_fp8"]
+            "sga_gemm_fp8", "sga_layer_fp8kv4_workspace_size", "sga_layer_forward_fp8kv4"]
 NOALLOC_SCRATCH_BYTES = 256 + 4 * 1024 * 1024
 KV4_ROW_BYTES = 416  # one row of the 4-bit latent cache (see sga_kv4_append)
 FP8_BLOCK = 128  # channels (and weight rows) that share a scale
@@ -65,6 +66,11 @@ class LayerWeights(ctypes.Structure):
     _fields_ = [("d_model", ctypes.c_int32), ("q_rank", ctypes.c_int32), ("w_hq", ctypes.c_void_p),
                 ("w_cq", ctypes.c_void_p), ("w_uk", ctypes.c_void_p), ("w_uv", ctypes.c_void_p),
                 ("w_o", ctypes.c_void_p)]
+
+
+class LayerFp8Weights(ctypes.Structure):
+    _fields_ = [("d_model", ctypes.c_int32), ("q_rank", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("w_hq", "w_hq_scale", "w_cq", "w_cq_scale", "w_o", "w_o_scale", "w_uk", "w_uv")]
 
 
 _lib = None
@@ -103,6 +109,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "sga_layer_project": (ctypes.c_int, [D, ctypes.POINTER(LayerWeights), P, P, P, P, P, P, P, P, P, sz, P]),
         "sga_layer_output": (ctypes.c_int, [D, ctypes.POINTER(LayerWeights), P, P, P, sz, P]),
         "sga_layer_forward": (ctypes.c_int, [D, ctypes.POINTER(LayerWeights), P, P, P, P, P, P, P, sz, P]),
+        "sga_layer_fp8kv4_workspace_size": (ctypes.c_int, [D, ctypes.POINTER(LayerFp8Weights), ctypes.POINTER(sz)]),
+        "sga_layer_forward_fp8kv4": (ctypes.c_int, [D, ctypes.POINTER(LayerFp8Weights), P, P, P, P, P, P, P, sz, P]),
         "sga_indexer_warmup_workspace_size": (ctypes.c_int, [D, ctypes.POINTER(sz)]),
         "sga_indexer_warmup": (ctypes.c_int, [D, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
         "sga_kv4_append": (ctypes.c_int, [D, P, P, P, P, sz, P]),
@@ -606,6 +614,60 @@ def layer_forward(wts, h, q_pos, kv_cache, k_idx_cache, top_k: int = TOP_K, idx_
     _check("sga_layer_forward", load_library().sga_layer_forward(
         ctypes.byref(dims), ctypes.byref(lw), _ptr(h), _ptr(q_pos), _ptr(kv_cache), _ptr(k_idx_cache),
         _ptr(idx_out), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
+    return idx_out, y
+
+
+def layer_fp8_weights(wts: dict) -> LayerFp8Weights:
+    """The C struct for the packed weights {w_hq, w_hq_scale, w_cq, w_cq_scale, w_o, w_o_scale, w_uk, w_uv} of
+    layer_forward_fp8kv4: E4M3 with fp32 block scales, w_uk and w_uv bf16 (see sga_layer_fp8_weights_t).  The tensors
+    must stay alive while the struct is in use."""
+    D, R = wts["w_hq"].shape[1], wts["w_cq"].shape[1]
+    hq_rows = -(-R // FP8_BLOCK) * FP8_BLOCK + HQ_EXTRA_FP8
+    for name, rows, cols in (("w_hq", hq_rows, D), ("w_cq", CQ_ROWS_FP8, R), ("w_o", D, HEADS * V_HEAD)):
+        _need_fp8(wts[name], name, (rows, cols))
+        _need(wts[name + "_scale"], name + "_scale", torch.float32, (-(-rows // FP8_BLOCK), -(-cols // FP8_BLOCK)))
+    _need(wts["w_uk"], "w_uk", torch.bfloat16, (HEADS, 128, V_DIM))
+    _need(wts["w_uv"], "w_uv", torch.bfloat16, (HEADS, V_HEAD, V_DIM))
+    return LayerFp8Weights(int(D), int(R), *(wts[n].data_ptr() for n, _ in LayerFp8Weights._fields_[2:]))
+
+
+def layer_fp8kv4_workspace_size(dims: Dims, lw: LayerFp8Weights) -> int:
+    out = ctypes.c_size_t(0)
+    _check("sga_layer_fp8kv4_workspace_size", load_library().sga_layer_fp8kv4_workspace_size(
+        ctypes.byref(dims), ctypes.byref(lw), ctypes.byref(out)))
+    return int(out.value)
+
+
+def alloc_layer_fp8kv4_workspace(dims: Dims, lw: LayerFp8Weights, device=None) -> torch.Tensor:
+    """A zero-filled workspace (ready for the first layer_forward_fp8kv4)."""
+    return torch.zeros(layer_fp8kv4_workspace_size(dims, lw), dtype=torch.uint8, device=device or "cuda")
+
+
+def layer_forward_fp8kv4(wts, h, q_pos, kv4, k_idx_cache, top_k: int = TOP_K, idx_out=None, y=None, ws=None,
+                         stream=None, return_idx: bool = True):
+    """One SGA layer on FP8 weights over the 4-bit latent cache (sga_layer_forward_fp8kv4).  Writes the new tokens'
+    cache rows in place; returns (idx [B,T,K] or None, y [B,T,D] fp32)."""
+    lw = layer_fp8_weights(wts)
+    B, T, _ = h.shape
+    L = kv4.shape[1]
+    _need(h, "h", torch.bfloat16, (B, T, lw.d_model))
+    _need(q_pos, "q_pos", torch.int32, (B, T))
+    _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
+    _need(k_idx_cache, "k_idx_cache", torch.bfloat16, (B, L, INDEX_DIM))
+    dims = make_dims(B, T, L, top_k)
+    if idx_out is None and return_idx:
+        idx_out = torch.empty((B, T, top_k), dtype=torch.int32, device=h.device)
+    if idx_out is not None:
+        _need(idx_out, "idx_out", torch.int32, (B, T, top_k))
+    if y is None:
+        y = torch.empty((B, T, lw.d_model), dtype=torch.float32, device=h.device)
+    _need(y, "y", torch.float32, (B, T, lw.d_model))
+    if ws is None:
+        ws = alloc_layer_fp8kv4_workspace(dims, lw, h.device)
+    _one_device(h, q_pos, kv4, k_idx_cache, idx_out, y, ws, *wts.values())
+    _check("sga_layer_forward_fp8kv4", load_library().sga_layer_forward_fp8kv4(
+        ctypes.byref(dims), ctypes.byref(lw), _ptr(h), _ptr(q_pos), _ptr(kv4), _ptr(k_idx_cache), _ptr(idx_out),
+        _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
     return idx_out, y
 
 

@@ -119,6 +119,7 @@ struct StreamParams {
   float* part;
   int* counters;
   int* status;
+  bool w_static;
 };
 
 // One thread block's part of one tile: units [u0, u1) of `units`.
@@ -198,33 +199,55 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_dependency_wait();
-  grid_launch_dependents();
+  if (warp != 0) {  // the producer waits in its own time
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
   const int begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-      int st = 0;
+      auto load_w = [&](int st, const Segment& sg, int u, int nkb) {
+        const uint32_t dst = ring + st * Cfg::kStageBytes;
+        for (int h = 0; h < nkb; ++h)
+          tma_load_2d(dst + h * kWBytes, &wmap, full(st), (kUnit * u + h) * kBlock, sg.mt * kTileM, pol_w);
+      };
+      auto load_x = [&](int st, const Segment& sg, int u, int nkb) {
+        const uint32_t dst = ring + st * Cfg::kStageBytes + kUnit * kWBytes;
+        for (int h = 0; h < nkb; ++h)
+          tma_load_2d(dst + h * Cfg::kXBytes, &xmap, full(st), (kUnit * u + h) * kBlock, sg.nb * NP, pol_x);
+      };
+      // Weights that no earlier kernel writes: the first stages of the first segment are loaded before waiting for it.
+      int pre = 0;
+      if (p.w_static) {
+        const Segment sg = segment_at(p, begin, end);
+        for (; pre < Cfg::kStages && sg.u0 + pre < sg.u1; ++pre) {
+          const int u = sg.u0 + pre, nkb = min(kUnit, p.k_blocks - kUnit * u);
+          mbar_arrive_expect_tx(full(pre), nkb * (kWBytes + Cfg::kXBytes));
+          load_w(pre, sg, u, nkb);
+        }
+      }
+      grid_dependency_wait();
+      grid_launch_dependents();
+      int st = 0, done = 0;
       uint32_t ph = 0;
       long long issued = 0;
       bool ok = true;
       for (int x = begin; x < end && ok;) {
         const Segment sg = segment_at(p, x, end);
-        for (int u = sg.u0; u < sg.u1; ++u) {
-          if (!mbar_wait(empty(st), ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+        for (int u = sg.u0; u < sg.u1; ++u, ++done) {
           const int nkb = min(kUnit, p.k_blocks - kUnit * u);
-          mbar_arrive_expect_tx(full(st), nkb * (kWBytes + Cfg::kXBytes));
-          const uint32_t dst = ring + st * Cfg::kStageBytes;
-          for (int h = 0; h < nkb; ++h) {
-            const int kb = kUnit * u + h;
-            tma_load_2d(dst + h * kWBytes, &wmap, full(st), kb * kBlock, sg.mt * kTileM, pol_w);
-            tma_load_2d(dst + kUnit * kWBytes + h * Cfg::kXBytes, &xmap, full(st), kb * kBlock, sg.nb * NP, pol_x);
+          if (done >= pre) {
+            if (!mbar_wait(empty(st), ph ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(full(st), nkb * (kWBytes + Cfg::kXBytes));
+            load_w(st, sg, u, nkb);
           }
+          load_x(st, sg, u, nkb);
           ++issued;
           if (++st == Cfg::kStages) {
             st = 0;
@@ -503,6 +526,7 @@ cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   p.part = host::at<float>(a.ws, kPartOff);
   p.counters = host::at<int>(a.ws, kCounterOff);
   p.status = a.status;
+  p.w_static = a.w_static;
   CUtensorMap wmap, xmap;
   cudaError_t e = make_tmap_2d(&wmap, true, a.w, a.k, a.m, a.k, kBlock, kTileM);
   if (e != cudaSuccess) return e;

@@ -118,6 +118,7 @@ struct GemmFp8Args {
   uint16_t* out_bf16;    // [n][m], or null
   void* ws;              // SGA_GEMM_FP8_WORKSPACE_BYTES, counters zero
   int* status;
+  bool w_static = false;  // no earlier kernel of the stream writes w: it may be read before they finish
 };
 cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int num_sms, cudaStream_t s);
 

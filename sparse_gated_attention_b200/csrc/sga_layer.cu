@@ -111,7 +111,7 @@ __device__ __forceinline__ void rope_rotate(float x, float y, float c, float s, 
 }
 
 struct PrepHArgs {
-  const float* g1;       // [splits][rows][R + 768] partial sums
+  const float* g1;       // [splits][rows][ld] partial sums: c_q, then c_kv and k_rope at off_kv, k_idx, w
   const int32_t* q_pos;  // [rows]
   uint16_t* c_q;         // [rows][R]
   uint16_t* kv_cache;    // [B][L][576]
@@ -121,6 +121,8 @@ struct PrepHArgs {
   int R, n_q, L, splits;
   size_t split_stride;   // elements between consecutive partial-sum arrays
   RopeFreqs freqs;
+  int ld, off_kv, off_kidx, off_w;
+  uint16_t* kv_rows;     // [rows][576]: the tokens' c_kv and k_rope go here instead of into kv_cache, or null
 };
 
 // The sum of a GEMM output's `splits` partials, in split order.
@@ -156,12 +158,11 @@ __global__ void layer_prep_h_kernel(PrepHArgs a) {
   const int row = blockIdx.x;
   const int b = row / a.n_q;
   const int pos = a.q_pos[row];
-  const int ld = a.R + kHqExtra;
-  const Partials g{a.g1 + static_cast<size_t>(row) * ld, a.splits, a.split_stride};
+  const Partials g{a.g1 + static_cast<size_t>(row) * a.ld, a.splits, a.split_stride};
   const bool cache = pos >= 0 && pos < a.L;
   if (!cache && threadIdx.x == 0 && blockIdx.y == 0) atomicCAS(a.status, 0, SGA_ERR_DEVICE_ARG);
   const size_t cache_row = static_cast<size_t>(b) * a.L + (cache ? pos : 0);
-  uint16_t* kv = a.kv_cache + cache_row * kKvDim;
+  uint16_t* kv = a.kv_rows ? a.kv_rows + static_cast<size_t>(row) * kKvDim : a.kv_cache + cache_row * kKvDim;
   uint16_t* ki = a.kidx_cache + cache_row * kIdxDim;
   // items: c_q (R) | w (64) | c_kv (512) | k_idx (128) | rope pairs (32)
   const int n_items = a.R + kIdxHeads + (cache ? kLatent + kIdxDim + kRope / 2 : 0);
@@ -173,29 +174,29 @@ __global__ void layer_prep_h_kernel(PrepHArgs a) {
     }
     j -= a.R;
     if (j < kIdxHeads) {
-      a.w[static_cast<size_t>(row) * kIdxHeads + j] = bf16_bits(g[a.R + kKvDim + kIdxDim + j]);
+      a.w[static_cast<size_t>(row) * kIdxHeads + j] = bf16_bits(g[a.off_w + j]);
       continue;
     }
     j -= kIdxHeads;
     if (j < kLatent) {
-      kv[j] = bf16_bits(g[a.R + j]);
+      kv[j] = bf16_bits(g[a.off_kv + j]);
       continue;
     }
     j -= kLatent;
     if (j < kIdxDim) {
-      ki[j] = bf16_bits(g[a.R + kKvDim + j]);
+      ki[j] = bf16_bits(g[a.off_kidx + j]);
       continue;
     }
     j -= kIdxDim;  // rope pair j
     float c, sn;
     rope_cs(pos, a.freqs.f[j], &c, &sn);
-    rope_rotate(g[a.R + kLatent + 2 * j], g[a.R + kLatent + 2 * j + 1], c, sn, &kv[kLatent + 2 * j],
+    rope_rotate(g[a.off_kv + kLatent + 2 * j], g[a.off_kv + kLatent + 2 * j + 1], c, sn, &kv[kLatent + 2 * j],
                 &kv[kLatent + 2 * j + 1]);
   }
 }
 
 struct PrepQArgs {
-  const float* g2;       // [splits][rows][20544] partial sums
+  const float* g2;       // [splits][rows][ld] partial sums: the query heads, the gate at 12,288, q_idx at off_qidx
   const int32_t* q_pos;  // [rows]
   uint16_t* q_nope;      // [rows][64][128]
   uint16_t* q;           // [rows][64][576]: rotated q_rope into dims 512..575
@@ -204,6 +205,7 @@ struct PrepQArgs {
   int splits;
   size_t split_stride;
   RopeFreqs freqs;
+  int ld, off_qidx;
 };
 
 // Blocks (token, part): q_nope, the rotated q_rope, the gate logits and the
@@ -216,7 +218,7 @@ __global__ void layer_prep_q_kernel(PrepQArgs a) {
   const int pos = a.q_pos[row];  // range-checked where the caches are written; only the angle uses it here
   if (threadIdx.x < kRope / 2) rope_cs(pos, a.freqs.f[threadIdx.x], &cs[threadIdx.x][0], &cs[threadIdx.x][1]);
   __syncthreads();
-  const Partials g{a.g2 + static_cast<size_t>(row) * kCqRows, a.splits, a.split_stride};
+  const Partials g{a.g2 + static_cast<size_t>(row) * a.ld, a.splits, a.split_stride};
   // items: q_nope (64 x 128) | rope pairs (64 x 32) | gate (64) | q_idx (64 x 128)
   constexpr int kItems = kHeads * kNope + kHeads * (kRope / 2) + kHeads + kIdxHeads * kIdxDim;
   for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < kItems; e += kPrepQParts * blockDim.x) {
@@ -240,7 +242,7 @@ __global__ void layer_prep_q_kernel(PrepQArgs a) {
       continue;
     }
     j -= kHeads;
-    a.q_idx[static_cast<size_t>(row) * kIdxHeads * kIdxDim + j] = bf16_bits(g[kQRows + kHeads + j]);
+    a.q_idx[static_cast<size_t>(row) * kIdxHeads * kIdxDim + j] = bf16_bits(g[a.off_qidx + j]);
   }
 }
 
@@ -398,7 +400,8 @@ sga_status_t project_impl(const sga_dims_t& d, const sga_layer_weights_t* W, con
                      nullptr, 0, 0, status};
     if ((e = sga::launch_gemm(ga, sms, s)) != cudaSuccess) return from_cuda(e);
     PrepHArgs pa{g1, q_pos, c_q, kv_cache, kidx_cache, w, status, R, d.n_q, d.kv_stride, l.splits.g1,
-                 static_cast<size_t>(rows) * (R + kHqExtra), rope_freqs()};
+                 static_cast<size_t>(rows) * (R + kHqExtra), rope_freqs(), R + kHqExtra, R, R + kKvDim,
+                 R + kKvDim + kIdxDim, nullptr};
     if ((e = launch_pdl(layer_prep_h_kernel, dim3(rows, kPrepHParts), s, pa)) != cudaSuccess) return from_cuda(e);
   }
   {
@@ -406,7 +409,8 @@ sga_status_t project_impl(const sga_dims_t& d, const sga_layer_weights_t* W, con
     // G2: [rows][20544] = c_q W_cq^T
     sga::GemmArgs ga{W->w_cq, c_q, kCqRows, rows, R, 1, false, R, 0, l.splits.g2, g2, nullptr, 0, 0, status};
     if ((e = sga::launch_gemm(ga, sms, s)) != cudaSuccess) return from_cuda(e);
-    PrepQArgs qa{g2, q_pos, q_nope, q, gate, q_idx, l.splits.g2, static_cast<size_t>(rows) * kCqRows, rope_freqs()};
+    PrepQArgs qa{g2,          q_pos, q_nope, q, gate, q_idx, l.splits.g2, static_cast<size_t>(rows) * kCqRows,
+                 rope_freqs(), kCqRows, kQRows + kHeads};
     if ((e = launch_pdl(layer_prep_q_kernel, dim3(rows, kPrepQParts), s, qa)) != cudaSuccess) return from_cuda(e);
   }
   sga::host::NvtxRange range("sga.layer.g3_uk");
@@ -460,9 +464,153 @@ sga_status_t check_layer_ws(void* ws, size_t ws_bytes, const sga_dims_t& d, cons
   return SGA_OK;
 }
 
+// ---------------------------------------------------------------- the layer in few bits
+// The same steps with the three large products (G1, G2, G5) on E4M3 weights with a scale per 128 x 128 block, their
+// inputs quantised per token and block of 128 just before, and the latent rows in the 4-bit cache.  In the packed
+// weights every matrix starts at a multiple of 128 rows, so that its own scale blocks stay whole.
+constexpr int kBlock8 = 128;
+int ceil_block8(int x) { return (x + kBlock8 - 1) / kBlock8 * kBlock8; }
+constexpr int kKvPad8 = 640;                                    // 576 rows of W_DKV
+constexpr int kHqExtra8 = kKvPad8 + kIdxDim + kIdxHeads;        // 832
+constexpr int kQIdxOff8 = kQRows + 128;                         // 64 rows of W_G
+constexpr int kCqRows8 = kQIdxOff8 + kIdxHeads * kIdxDim;       // 20,608
+
+struct LayerLayout8 {
+  size_t path_bytes = 0;  // sga_forward_kv4's workspace, at the start (its status word is the layer's)
+  size_t gemm = 0, codes = 0, scale = 0, g1 = 0, c_q = 0, g2 = 0, q_nope = 0, q = 0, gate = 0, q_idx = 0, w = 0;
+  size_t kv_rows = 0, out_b = 0, o_b = 0, total = 0;
+};
+
+bool layer_dims_ok8(const sga_dims_t* d, const sga_layer_fp8_weights_t* W) {
+  if (!d || !W) return false;
+  if (d->batch < 1 || d->n_q < 1 || d->kv_stride < 1 || d->kv_stride > SGA_MAX_KV_STRIDE) return false;
+  if (d->top_k < 64 || d->top_k > SGA_MAX_TOP_K || d->top_k % 64 != 0) return false;
+  if (W->d_model < 16 || W->d_model % 16 != 0 || W->q_rank < 16 || W->q_rank % 16 != 0) return false;
+  const long long rows = static_cast<long long>(d->batch) * d->n_q;
+  if (rows * kHeads * kLatent > INT32_MAX || rows * (W->q_rank + kBlock8 + kHqExtra8) > INT32_MAX) return false;
+  return static_cast<long long>(d->batch) * d->kv_stride <= INT32_MAX;
+}
+
+sga_status_t layer_layout8(const sga_dims_t& d, int d_model, int q_rank, LayerLayout8* l) {
+  const size_t rows = static_cast<size_t>(d.batch) * d.n_q;
+  const sga_status_t st = sga_workspace_size(&d, SGA_OP_FORWARD, &l->path_bytes);
+  if (st != SGA_OK) return st;
+  size_t off = align_up(l->path_bytes);
+  const auto take = [&](size_t bytes) {
+    const size_t at_off = off;
+    off += align_up(bytes);
+    return at_off;
+  };
+  const size_t widest = std::max<size_t>(std::max(d_model, q_rank), kOWidth);
+  l->gemm = take(SGA_GEMM_FP8_WORKSPACE_BYTES);
+  l->codes = take(rows * widest);
+  l->scale = take(rows * ((widest + kBlock8 - 1) / kBlock8) * 4);
+  l->g1 = take(rows * (ceil_block8(q_rank) + kHqExtra8) * 4);
+  l->c_q = take(rows * q_rank * 2);
+  l->g2 = take(rows * kCqRows8 * 4);
+  l->q_nope = take(rows * kHeads * kNope * 2);
+  l->q = take(rows * kHeads * kKvDim * 2);
+  l->gate = take(rows * kHeads * 2);
+  l->q_idx = take(rows * kIdxHeads * kIdxDim * 2);
+  l->w = take(rows * kIdxHeads * 2);
+  l->kv_rows = take(rows * kKvDim * 2);
+  l->out_b = take(rows * kHeads * kLatent * 2);
+  l->o_b = take(rows * kOWidth * 2);
+  l->total = off;
+  return SGA_OK;
+}
+
+// y[rows][m] = x w^T for bf16 x [rows][k]: quantised into the workspace, then the block-scaled product.
+cudaError_t quantized_product(const uint16_t* x, int rows, int k, const sga_fp8_e4m3_t* w, const float* w_scale, int m,
+                              float* y, void* ws, const LayerLayout8& l, int sms, cudaStream_t s) {
+  uint8_t* codes = at<uint8_t>(ws, l.codes);
+  float* scale = at<float>(ws, l.scale);
+  const cudaError_t e = sga::launch_quantize_fp8(rows, k, x, codes, scale, s);
+  if (e != cudaSuccess) return e;
+  sga::GemmFp8Args a{rows, m, k, codes, scale, w, w_scale, y, nullptr, at<void>(ws, l.gemm), at<int>(ws, 0)};
+  a.w_static = true;
+  return sga::launch_gemm_fp8(a, sms, s);
+}
+
 }  // namespace
 
 extern "C" {
+
+sga_status_t sga_layer_fp8kv4_workspace_size(const sga_dims_t* dims, const sga_layer_fp8_weights_t* weights,
+                                             size_t* bytes) {
+  if (!bytes || !layer_dims_ok8(dims, weights)) return SGA_ERR_INVALID_ARG;
+  LayerLayout8 l;
+  const sga_status_t st = layer_layout8(*dims, weights->d_model, weights->q_rank, &l);
+  if (st != SGA_OK) return st;
+  *bytes = l.total;
+  return SGA_OK;
+}
+
+sga_status_t sga_layer_forward_fp8kv4(const sga_dims_t* dims, const sga_layer_fp8_weights_t* W, const sga_bf16_t* h,
+                                      const int32_t* q_pos, uint8_t* kv4, sga_bf16_t* k_idx_cache, int32_t* idx_out,
+                                      float* y, void* ws, size_t ws_bytes, sga_stream_t stream) {
+  if (!layer_dims_ok8(dims, W)) return SGA_ERR_INVALID_ARG;
+  if (!aligned(W->w_hq, 16) || !aligned(W->w_cq, 16) || !aligned(W->w_o, 16) || !aligned(W->w_uk, 16) ||
+      !aligned(W->w_uv, 16) || !aligned(W->w_hq_scale, 4) || !aligned(W->w_cq_scale, 4) || !aligned(W->w_o_scale, 4))
+    return SGA_ERR_INVALID_ARG;
+  if (!aligned(h, 16) || !aligned(q_pos, 4) || !aligned(kv4, 16) || !aligned(k_idx_cache, 16) || !aligned(y, 16) ||
+      (idx_out && !aligned(idx_out, 16)))
+    return SGA_ERR_INVALID_ARG;
+  LayerLayout8 l;
+  sga_status_t st = layer_layout8(*dims, W->d_model, W->q_rank, &l);
+  if (st != SGA_OK) return st;
+  if (!aligned(ws, kAlign) || ws_bytes < l.total) return SGA_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = device_info(&sms)) != SGA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int rows = dims->batch * dims->n_q, R = W->q_rank, Rp = ceil_block8(R), ld1 = Rp + kHqExtra8;
+  int* status = at<int>(ws, 0);
+  float* g1 = at<float>(ws, l.g1);
+  float* g2 = at<float>(ws, l.g2);
+  uint16_t* c_q = at<uint16_t>(ws, l.c_q);
+  uint16_t* q_nope = at<uint16_t>(ws, l.q_nope);
+  uint16_t* q = at<uint16_t>(ws, l.q);
+  uint16_t* gate = at<uint16_t>(ws, l.gate);
+  uint16_t* q_idx = at<uint16_t>(ws, l.q_idx);
+  uint16_t* w = at<uint16_t>(ws, l.w);
+  uint16_t* kv_rows = at<uint16_t>(ws, l.kv_rows);
+  uint16_t* out_b = at<uint16_t>(ws, l.out_b);
+  uint16_t* o_b = at<uint16_t>(ws, l.o_b);
+  cudaError_t e;
+  {
+    sga::host::NvtxRange range("sga.layer.g1_hq");
+    e = quantized_product(h, rows, W->d_model, W->w_hq, W->w_hq_scale, ld1, g1, ws, l, sms, s);
+    if (e != cudaSuccess) return from_cuda(e);
+    PrepHArgs pa{g1, q_pos, c_q, nullptr, k_idx_cache, w, status, R, dims->n_q, dims->kv_stride, 1, 0, rope_freqs(),
+                 ld1, Rp, Rp + kKvPad8, Rp + kKvPad8 + kIdxDim, kv_rows};
+    if ((e = launch_pdl(layer_prep_h_kernel, dim3(rows, kPrepHParts), s, pa)) != cudaSuccess) return from_cuda(e);
+    e = sga::launch_kv4_append(kv_rows, q_pos, kv4, status, dims->batch, dims->n_q, dims->kv_stride, s);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  {
+    sga::host::NvtxRange range("sga.layer.g2_cq");
+    e = quantized_product(c_q, rows, R, W->w_cq, W->w_cq_scale, kCqRows8, g2, ws, l, sms, s);
+    if (e != cudaSuccess) return from_cuda(e);
+    PrepQArgs qa{g2, q_pos, q_nope, q, gate, q_idx, 1, 0, rope_freqs(), kCqRows8, kQIdxOff8};
+    if ((e = launch_pdl(layer_prep_q_kernel, dim3(rows, kPrepQParts), s, qa)) != cudaSuccess) return from_cuda(e);
+  }
+  {
+    sga::host::NvtxRange range("sga.layer.g3_uk");
+    sga::GemmArgs ga{W->w_uk, q_nope, kLatent, rows, kNope, kHeads, true, kHeads * kNope, kNope, 1, nullptr, q,
+                     kHeads * kKvDim, kKvDim, status};
+    if ((e = sga::launch_gemm(ga, sms, s)) != cudaSuccess) return from_cuda(e);
+  }
+  st = sga_forward_kv4(dims, q_idx, w, k_idx_cache, q, kv4, gate, q_pos, idx_out, out_b, ws, l.path_bytes, stream);
+  if (st != SGA_OK) return st;
+  {
+    sga::host::NvtxRange range("sga.layer.g4_uv");
+    sga::GemmArgs ga{W->w_uv, out_b, kVHead, rows, kLatent, kHeads, false, kHeads * kLatent, kLatent, 1, nullptr, o_b,
+                     kOWidth, kVHead, status};
+    if ((e = sga::launch_gemm(ga, sms, s)) != cudaSuccess) return from_cuda(e);
+  }
+  sga::host::NvtxRange range("sga.layer.g5_o");
+  return from_cuda(quantized_product(o_b, rows, kOWidth, W->w_o, W->w_o_scale, W->d_model, y, ws, l, sms, s));
+}
 
 sga_status_t sga_layer_workspace_size(const sga_dims_t* dims, const sga_layer_weights_t* weights, sga_layer_op_t op,
                                       size_t* bytes) {

@@ -504,6 +504,89 @@ def test_two_streams_at_once_with_their_own_workspaces():
             assert torch.equal(y, want[i])
 
 
+# ------------------------------------------------------------------------------------------------ the layer
+def fp8_weight(g, rows, cols):
+    """Rows x cols of N(0, 1) / sqrt(cols) as E4M3 codes with a scale per 128 x 128 block."""
+    w = randn(g, rows, cols) * cols ** -0.5
+    rb, cb = -(-rows // 128), -(-cols // 128)
+    pad = torch.zeros((rb * 128, cb * 128), device=DEV)
+    pad[:rows, :cols] = w
+    blocks = pad.view(rb, 128, cb, 128)
+    scale = blocks.abs().amax((1, 3)).clamp_min(1e-9) / 448.0
+    codes = (blocks / scale[:, None, :, None]).clamp(-448, 448).view(rb * 128, cb * 128)[:rows, :cols]
+    return codes.to(torch.float8_e4m3fn).contiguous(), scale.contiguous()
+
+
+def fp8_layer_weights(D, R, seed=0):
+    g = gen(seed)
+    wts = {}
+    for name, rows, cols in (("w_hq", -(-R // 128) * 128 + 832, D), ("w_cq", 20608, R), ("w_o", D, 8192)):
+        wts[name], wts[name + "_scale"] = fp8_weight(g, rows, cols)
+    for name in ("w_uk", "w_uv"):
+        wts[name] = (randn(g, 64, 128, 512) * 512 ** -0.5).to(torch.bfloat16)
+    return wts
+
+
+@pytest.mark.parametrize("D,R,B,T,L,pos", [(7168, 1536, 2, 1, 1500, [[1499], [600]]),
+                                           (1040, 400, 2, 3, 300, [[0, 5, 299], [100, 101, 102]]),
+                                           (512, 144, 1, 140, 200, None)])
+def test_layer_fp8kv4_matches_definition(D, R, B, T, L, pos):
+    """Contexts of at most 2048: the selection keeps every position (exact indices).  The caches' new rows: the key
+    row within one bf16 place, the 4-bit row's codes equal but for a few (an fp32 sum next to a rounding border).  y as
+    for the bf16 layer: four bf16 rounding stages, within rel-L2 1e-2; an activation that rounds the other way
+    changes an E4M3 code now and then, by a step of 2^-3 in one of thousands of addends."""
+    wts = fp8_layer_weights(D, R, seed=D)
+    g = gen(D + 1)
+    h = randn(g, B, T, D).to(torch.bfloat16)
+    if pos is None:
+        pos = [list(range(30, 30 + T))] * B
+    q_pos = torch.tensor(pos, dtype=torch.int32, device=DEV)
+    cache, k_idx = fill_cache(g, B, L), randn(g, B, L, 128).to(torch.bfloat16)
+    cache0, k_idx0 = cache.clone(), k_idx.clone()
+    lw = sga.layer_fp8_weights(wts)
+    ws = sga.alloc_layer_fp8kv4_workspace(sga.make_dims(B, T, L), lw)
+    idx, y = sga.layer_forward_fp8kv4(wts, h, q_pos, cache, k_idx, ws=ws)
+    assert sga.device_status(ws) == 0
+    want = lowbit.layer_forward(h, q_pos, cache0, k_idx0, wts)
+    np.testing.assert_array_equal(idx.cpu().numpy(), want["idx"])
+    new = torch.zeros((B, L), dtype=torch.bool, device=DEV)
+    new.scatter_(1, q_pos.long(), True)
+    assert torch.equal(cache[~new], cache0[~new]) and torch.equal(k_idx[~new], k_idx0[~new])
+    got_rows, want_rows = cache[new].cpu().numpy(), want["packed"][new.cpu().numpy()]
+    assert float(np.mean(got_rows != want_rows)) < 1e-2
+    gk, wk = lowbit.to_f64(k_idx)[new.cpu().numpy()], want["k_idx"][new.cpu().numpy()]
+    assert (np.abs(gk - wk) <= 2.0 ** -7 * np.abs(wk) + 1e-5).all()
+    got = lowbit.to_f64(y)
+    rel = np.linalg.norm(got - want["y"]) / np.linalg.norm(want["y"])
+    assert rel <= 1e-2, f"rel-L2 {rel:.3e}"
+    # again on the same workspace and caches, and replayed from a graph: the same bits
+    for _ in range(2):
+        idx2, y2 = sga.layer_forward_fp8kv4(wts, h, q_pos, cache, k_idx, ws=ws)
+        assert torch.equal(idx2, idx) and torch.equal(y2, y)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        idx3, y3 = sga.layer_forward_fp8kv4(wts, h, q_pos, cache, k_idx, ws=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(idx3, idx) and torch.equal(y3, y)
+
+
+def test_layer_fp8kv4_position_out_of_range_is_reported():
+    wts = fp8_layer_weights(256, 144, seed=5)
+    g = gen(6)
+    h = randn(g, 2, 1, 256).to(torch.bfloat16)
+    cache, k_idx = fill_cache(g, 2, 100), randn(g, 2, 100, 128).to(torch.bfloat16)
+    cache0, k_idx0 = cache.clone(), k_idx.clone()
+    q_pos = torch.tensor([[100], [50]], dtype=torch.int32, device=DEV)
+    ws = sga.alloc_layer_fp8kv4_workspace(sga.make_dims(2, 1, 100), sga.layer_fp8_weights(wts))
+    sga.layer_forward_fp8kv4(wts, h, q_pos, cache, k_idx, ws=ws)
+    assert sga.device_status(ws) == 6
+    assert torch.equal(cache[0], cache0[0]) and torch.equal(k_idx[0], k_idx0[0])
+    assert not torch.equal(cache[1, 50], cache0[1, 50])
+
+
 # ------------------------------------------------------------------------------------------------ refusals
 def test_python_refusals():
     x, xs, w, wsc = product_case(4, 64, 256, 30)

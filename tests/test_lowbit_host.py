@@ -155,3 +155,31 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
     with pytest.raises(ValueError, match="CUDA tensor"):
         sga.sparse_mla_attend_kv4(torch.zeros((1, 1, 64, 576), dtype=bf), torch.zeros((1, 8, 416), dtype=u8),
                                   torch.zeros((1, 1, 64), dtype=i32))
+
+
+def _fp8_weights(d_model=7168, q_rank=1536, **bad):
+    names = ("w_hq", "w_hq_scale", "w_cq", "w_cq_scale", "w_o", "w_o_scale", "w_uk", "w_uv")
+    return sga.LayerFp8Weights(d_model, q_rank, *(bad.get(n, 0x300000 + 0x100000 * i) for i, n in enumerate(names)))
+
+
+def test_layer_fp8kv4_workspace_and_refusals(lib):
+    d = sga.make_dims(32, 1, 131072)
+    size = sga.layer_fp8kv4_workspace_size(d, _fp8_weights())
+    assert size >= sga.workspace_size(d) + sga.GEMM_FP8_WORKSPACE_BYTES + 32 * 4 * (20608 + 1536 + 832)
+    r, big = ctypes.byref(d), 1 << 40
+
+    def call(W=_fp8_weights(), dims=r, h=GOOD, pos=GOOD, kv4=GOOD, k=GOOD, idx=None, y=GOOD, ws=WS, nbytes=big):
+        return lib.sga_layer_forward_fp8kv4(dims, ctypes.byref(W), h, pos, kv4, k, idx, y, ws, nbytes, None)
+
+    for W in (_fp8_weights(d_model=7160), _fp8_weights(q_rank=1528), _fp8_weights(d_model=0), _fp8_weights(w_hq=0),
+              _fp8_weights(w_cq=0x400008), _fp8_weights(w_o_scale=0), _fp8_weights(w_hq_scale=0x500002),
+              _fp8_weights(w_uk=2), _fp8_weights(w_uv=0)):
+        assert call(W=W) == 1
+    for bad in (dict(h=ODD), dict(pos=None), dict(kv4=P(0x100008)), dict(k=ODD), dict(idx=ODD), dict(y=None)):
+        assert call(**bad) == 1, bad
+    assert call(dims=ctypes.byref(sga.make_dims(1, 1, 100, 65))) == 1
+    for bad in (dict(ws=None), dict(ws=P(0x20000010)), dict(nbytes=size - 1)):
+        assert call(**bad) == 3, bad
+    out = ctypes.c_size_t(0)
+    assert lib.sga_layer_fp8kv4_workspace_size(r, None, ctypes.byref(out)) == 1
+    assert lib.sga_layer_fp8kv4_workspace_size(r, ctypes.byref(_fp8_weights()), None) == 1
