@@ -89,11 +89,7 @@ constexpr int kUnit = 2;                        // K blocks per ring stage
 constexpr int kChunk = 16;                      // K blocks per scale slot
 constexpr int kStreamThreads = 256;             // warps: TMA, MMA, 2 of scales, 4 of accumulation
 constexpr int kAccBufs = 4;
-constexpr int kMaxGrid = 148;                   // thread blocks (ranges); sizes the workspace
-constexpr size_t kCounterOff = host::kStatusBytes;
-constexpr size_t kPartOff = kCounterOff + 1024;
-static_assert(kMaxGrid * 4 <= 1024, "counters");
-static_assert(kPartOff + sizeof(float) * kMaxGrid * 2 * kTileM * 128 <= SGA_GEMM_FP8_WORKSPACE_BYTES, "workspace");
+constexpr int kMaxSplits = 8;                   // thread blocks of a cluster
 
 template <int NP>
 struct StreamCfg {
@@ -104,47 +100,28 @@ struct StreamCfg {
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 4 + 1;
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kScaleBytes + kNumBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
+  // the partial sums of a split tile, 128 rows x NP tokens, lie over the ring
+  static_assert(kStages * kStageBytes >= 4 * kTileM * (NP + kMaxSplits), "receive buffer");
 };
 
 struct StreamParams {
-  int n, m, n_blocks, k_blocks, units;  // units: pairs of K blocks in a tile
-  int total;                            // units of all tiles
-  // Thread block c's range of units.  splits > 0: the (c % splits)-th of `splits` parts of tile c / splits; else one
-  // of gridDim.x equal ranges over all tiles, `base` units and one more for the first `more` of them.
-  int splits, base, more;
+  int n, m, tiles, k_blocks, units;  // units: pairs of K blocks in a tile
+  int splits;                        // thread blocks (a cluster) that share a tile's K
   const float* x_scale;
   const float* w_scale;
   float* out_f32;
   uint16_t* out_bf16;
-  float* part;
-  int* counters;
   int* status;
   bool w_static;
 };
 
-// One thread block's part of one tile: units [u0, u1) of `units`.
-struct Segment {
-  int tile, mt, nb, u0, u1;
-};
-
-__device__ __forceinline__ int range_begin(const StreamParams& p, int c) {
-  if (p.splits > 0) return c / p.splits * p.units + p.units * (c % p.splits) / p.splits;
-  return c * p.base + min(c, p.more);
-}
-// The thread block whose range holds unit x.
-__device__ __forceinline__ int range_of(const StreamParams& p, int x) {
-  const int cut = p.more * (p.base + 1);
-  return x < cut ? x / (p.base + 1) : p.more + (x - cut) / p.base;
-}
-
-__device__ __forceinline__ Segment segment_at(const StreamParams& p, int x, int end) {
-  Segment s;
-  s.tile = x / p.units;
-  s.u0 = x - s.tile * p.units;
-  s.u1 = min(p.units, s.u0 + (end - x));
-  s.mt = s.tile / p.n_blocks;
-  s.nb = s.tile - s.mt * p.n_blocks;
-  return s;
+__device__ __forceinline__ void store_y(const StreamParams& p, int row, int token, float v) {
+  const size_t i = static_cast<size_t>(token) * p.m + row;
+  if (p.out_bf16) {
+    p.out_bf16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  } else {
+    p.out_f32[i] = v;
+  }
 }
 
 template <int NP>
@@ -167,9 +144,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const uint32_t done_bar = bar0 + 8u * (2 * Cfg::kStages + 2 * kAccBufs + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
+  // This thread block's tiles (weight rows 128 t ..) and its part [u0, u1) of each one's K.
+  const int rank = blockIdx.x % p.splits;
+  const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  const int u0 = p.units * rank / p.splits, u1 = p.units * (rank + 1) / p.splits;
+  const int kb_end = min(kUnit * u1, p.k_blocks);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
@@ -203,58 +184,58 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
   }
-  const int begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-      auto load_w = [&](int st, const Segment& sg, int u, int nkb) {
+      const auto blocks_of = [&](int u) { return min(kUnit, p.k_blocks - kUnit * u); };
+      auto load_w = [&](int st, int t, int u) {
         const uint32_t dst = ring + st * Cfg::kStageBytes;
-        for (int h = 0; h < nkb; ++h)
-          tma_load_2d(dst + h * kWBytes, &wmap, full(st), (kUnit * u + h) * kBlock, sg.mt * kTileM, pol_w);
+        for (int h = 0; h < blocks_of(u); ++h)
+          tma_load_2d(dst + h * kWBytes, &wmap, full(st), (kUnit * u + h) * kBlock, t * kTileM, pol_w);
       };
-      auto load_x = [&](int st, const Segment& sg, int u, int nkb) {
+      auto load_x = [&](int st, int u) {
         const uint32_t dst = ring + st * Cfg::kStageBytes + kUnit * kWBytes;
-        for (int h = 0; h < nkb; ++h)
-          tma_load_2d(dst + h * Cfg::kXBytes, &xmap, full(st), (kUnit * u + h) * kBlock, sg.nb * NP, pol_x);
+        for (int h = 0; h < blocks_of(u); ++h)
+          tma_load_2d(dst + h * Cfg::kXBytes, &xmap, full(st), (kUnit * u + h) * kBlock, 0, pol_x);
       };
-      // Weights that no earlier kernel writes: the first stages of the first segment are loaded before waiting for it.
+      // While the kernel before this one runs: weights that it cannot write are loaded into the first stages; others
+      // are only brought into L2, which holds whatever it writes.
       int pre = 0;
-      if (p.w_static) {
-        const Segment sg = segment_at(p, begin, end);
-        for (; pre < Cfg::kStages && sg.u0 + pre < sg.u1; ++pre) {
-          const int u = sg.u0 + pre, nkb = min(kUnit, p.k_blocks - kUnit * u);
-          mbar_arrive_expect_tx(full(pre), nkb * (kWBytes + Cfg::kXBytes));
-          load_w(pre, sg, u, nkb);
+      for (; pre < Cfg::kStages && u0 + pre < u1; ++pre) {
+        if (p.w_static) {
+          mbar_arrive_expect_tx(full(pre), blocks_of(u0 + pre) * (kWBytes + Cfg::kXBytes));
+          load_w(pre, first, u0 + pre);
+        } else {
+          for (int h = 0; h < blocks_of(u0 + pre); ++h)
+            tma_prefetch_2d(&wmap, (kUnit * (u0 + pre) + h) * kBlock, first * kTileM);
         }
       }
+      if (!p.w_static) pre = 0;
       grid_dependency_wait();
       grid_launch_dependents();
-      int st = 0, done = 0;
+      int st = 0, n_done = 0;
       uint32_t ph = 0;
       long long issued = 0;
       bool ok = true;
-      for (int x = begin; x < end && ok;) {
-        const Segment sg = segment_at(p, x, end);
-        for (int u = sg.u0; u < sg.u1; ++u, ++done) {
-          const int nkb = min(kUnit, p.k_blocks - kUnit * u);
-          if (done >= pre) {
+      for (int t = first; t < p.tiles && ok; t += step) {
+        for (int u = u0; u < u1; ++u, ++n_done) {
+          if (n_done >= pre) {
             if (!mbar_wait(empty(st), ph ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(full(st), nkb * (kWBytes + Cfg::kXBytes));
-            load_w(st, sg, u, nkb);
+            mbar_arrive_expect_tx(full(st), blocks_of(u) * (kWBytes + Cfg::kXBytes));
+            load_w(st, t, u);
           }
-          load_x(st, sg, u, nkb);
+          load_x(st, u);
           ++issued;
           if (++st == Cfg::kStages) {
             st = 0;
             ph ^= 1u;
           }
         }
-        x += sg.u1 - sg.u0;
       }
       if (!ok) {
         record_status(p.status, kStatusTimeout);
@@ -264,6 +245,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           mbar_wait(full(static_cast<int>(i % Cfg::kStages)), static_cast<uint32_t>((i / Cfg::kStages) & 1), &never);
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -272,9 +254,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int st = 0, buf = 0;
     uint32_t ph = 0, aph = 0;
     bool ok = true;
-    for (int x = begin; x < end && ok;) {
-      const Segment sg = segment_at(p, x, end);
-      for (int u = sg.u0; u < sg.u1 && ok; ++u) {
+    for (int t = first; t < p.tiles && ok; t += step) {
+      for (int u = u0; u < u1 && ok; ++u) {
         ok = __all_sync(kAll, mbar_wait(full(st), ph, abort_flag));
         if (!ok) break;
         const int nkb = min(kUnit, p.k_blocks - kUnit * u);
@@ -304,7 +285,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           ph ^= 1u;
         }
       }
-      x += sg.u1 - sg.u0;
     }
     if (!ok && lane == 0) {
       record_status(p.status, kStatusTimeout);
@@ -313,43 +293,43 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     if (elect_one()) mma_commit(done_bar);
     __syncwarp();
     volatile int never = 0;
-    mbar_wait(done_bar, 0, &never);  // every MMA has finished before TMEM is freed
+    mbar_wait(done_bar, 0, &never);  // every MMA has finished before TMEM is freed and the ring reused
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales
     // Products x_scale * w_scale of up to 16 K blocks at a time, two slots.
-    const int t = threadIdx.x - 64;
+    const int t64 = threadIdx.x - 64;
     int slot = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int x = begin; x < end && ok;) {
-      const Segment sg = segment_at(p, x, end);
-      const float* ws = p.w_scale + static_cast<size_t>(sg.mt) * p.k_blocks;
-      for (int kb0 = kUnit * sg.u0; kb0 < kUnit * sg.u1; kb0 += kChunk) {
+    for (int t = first; t < p.tiles && ok; t += step) {
+      const float* ws = p.w_scale + static_cast<size_t>(t) * p.k_blocks;
+      for (int kb0 = kUnit * u0; kb0 < kb_end; kb0 += kChunk) {
+        // this thread's K block and every fourth token, all loads before the first store (addresses past the end are
+        // clamped: their products scale zeros or go unused)
+        const int kbl = t64 % kChunk, tok0 = t64 / kChunk, kb = min(kb0 + kbl, p.k_blocks - 1);
+        const float wv = __ldg(ws + kb);
+        float v[NP / 4];
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i)
+          v[i] = __ldg(p.x_scale + static_cast<size_t>(min(tok0 + 4 * i, p.n - 1)) * p.k_blocks + kb);
         if (!mbar_wait(sempty(slot), ph ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
         float* dst = scales + slot * kChunk * NP;
-        // this thread's K block and every fourth token, all loads before the first store (addresses past the end are
-        // clamped: their products scale zeros or go unused)
-        const int kbl = t % kChunk, tok0 = t / kChunk, kb = min(kb0 + kbl, p.k_blocks - 1);
-        const float wv = __ldg(ws + kb);
-        float v[NP / 4];
-#pragma unroll
-        for (int i = 0; i < NP / 4; ++i)
-          v[i] = __ldg(p.x_scale + static_cast<size_t>(min(sg.nb * NP + tok0 + 4 * i, p.n - 1)) * p.k_blocks + kb);
 #pragma unroll
         for (int i = 0; i < NP / 4; ++i) dst[kbl * NP + tok0 + 4 * i] = v[i] * wv;
         mbar_arrive(sfull(slot));
         slot ^= 1;
         if (slot == 0) ph ^= 1u;
       }
-      x += sg.u1 - sg.u0;
     }
     if (!ok) {
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ scaled accumulation
     // Warp w reads TMEM lane quarter w % 4: this thread's weight row is 32 (w % 4) + lane of the tile, its
@@ -360,14 +340,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int buf = 0, slot = 0;
     uint32_t aph = 0, sph = 0;
     bool ok = true;
-    for (int x = begin; x < end && ok;) {
-      const Segment sg = segment_at(p, x, end);
-      x += sg.u1 - sg.u0;
-      float acc[NP];
+    float acc[NP];
+    for (int t = first; t < p.tiles && ok; t += step) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) acc[i] = 0.f;
-      const int kb_end = min(kUnit * sg.u1, p.k_blocks);
-      for (int kb0 = kUnit * sg.u0; kb0 < kb_end && ok; kb0 += kChunk) {
+      for (int kb0 = kUnit * u0; kb0 < kb_end && ok; kb0 += kChunk) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(sfull(slot), sph, abort_flag));
         if (!ok) break;
         const float* sc = scales + slot * kChunk * NP;
@@ -408,74 +385,47 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         slot ^= 1;
         if (slot == 0) sph ^= 1u;
       }
-      ok = !named_barrier_or(1, 128, !ok);  // all four warps write, or none
-      if (!ok) break;
-      bool write = true;
-      if (sg.u0 != 0 || sg.u1 != p.units) {
-        // A shared tile: leave the partial sums, and let the last of the tile's ranges add them all in order.
-        const int t0 = sg.tile * p.units;
-        const int c0 = p.splits > 0 ? sg.tile * p.splits : range_of(p, t0);  // the tile's first range, and its last
-        const int c1 = p.splits > 0 ? c0 + p.splits - 1 : range_of(p, t0 + p.units - 1);
-        auto part_of = [&](int c) {
-          const int second = range_begin(p, c) / p.units != sg.tile;  // a range's first tile, or its last
-          return p.part + (static_cast<size_t>(2 * c + second) * NP) * kTileM + mrow;
-        };
-        float* mine = part_of(blockIdx.x);
+      const int row = t * kTileM + mrow;
+      if (ok && p.splits == 1 && row < p.m) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) mine[i * kTileM] = acc[i];
-        named_barrier(1, 128);
-        if (threadIdx.x == 128) {
-          __threadfence();  // after the barrier: covers every thread's partial sums
-          const int before = atomicAdd(p.counters + c0, 1);
-          *last_flag = before == c1 - c0;
-          if (before == c1 - c0) p.counters[c0] = 0;
-          __threadfence();
-        }
-        named_barrier(1, 128);
-        write = *last_flag != 0;
-        if (write) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) acc[i] = 0.f;
-          // 128 loads a thread in flight (several ranges at a time for few tokens), added in range order
-          constexpr int kAtOnce = 128 / NP;
-          for (int c = c0; c <= c1; c += kAtOnce) {
-            float v[kAtOnce][NP];
-#pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
-              const float* from = part_of(min(c + q, c1));
-#pragma unroll
-              for (int i = 0; i < NP; ++i) v[q][i] = __ldcg(from + i * kTileM);
-            }
-#pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
-              if (c + q > c1) break;
-#pragma unroll
-              for (int i = 0; i < NP; ++i) acc[i] += v[q][i];
-            }
-          }
-        }
-        named_barrier(1, 128);  // last_flag read by all before the next tile writes it
-      }
-      const int row = sg.mt * kTileM + mrow;
-      if (write && row < p.m) {
-        const int tok0 = sg.nb * NP;
-        const size_t at0 = static_cast<size_t>(tok0) * p.m + row;
-        const int cols = min(NP, p.n - tok0);
-        if (p.out_bf16) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-            if (i < cols) p.out_bf16[at0 + static_cast<size_t>(i) * p.m] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-            if (i < cols) p.out_f32[at0 + static_cast<size_t>(i) * p.m] = acc[i];
-        }
+        for (int i = 0; i < NP; ++i)
+          if (i < p.n) store_y(p, row, i, acc[i]);
       }
     }
-    if (!ok) {
+    if (!ok && lane == 0) {
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
     }
+    __syncwarp();
+    if (p.splits > 1) {
+      // A tile shared by the cluster (its only one): thread block r sums tokens [NP r / S, NP (r + 1) / S) over the
+      // ranks in order.  Each sends its partial sums of those tokens to r, into the idle ring.
+      cluster_barrier();  // every MMA of the cluster has finished
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r) {
+        if (r >= p.splits) break;
+        const int c0 = NP * r / p.splits, c1 = NP * (r + 1) / p.splits;
+        const uint32_t dst = map_to_rank(ring, r) + 4u * ((rank * (c1 - c0) - c0) * kTileM + mrow);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          if (i >= c0 && i < c1) st_cluster(dst + 4u * i * kTileM, acc[i]);
+      }
+      cluster_barrier();
+      const int c0 = NP * rank / p.splits, c1 = NP * (rank + 1) / p.splits;
+      const int row = first * kTileM + mrow;
+      const float* part = reinterpret_cast<const float*>(smem) + mrow;
+      if (ok && row < p.m) {
+        for (int i = c0; i < c1 && i < p.n; ++i) {
+          float sum = 0.f;
+          for (int r = 0; r < p.splits; ++r) sum += part[(r * (c1 - c0) + i - c0) * kTileM];
+          store_y(p, row, i, sum);
+        }
+      }
+    }
+  }
+  if (warp < 4 && p.splits > 1) {
+    cluster_barrier();
+    cluster_barrier();
   }
 
   tc_fence_before();
@@ -486,45 +436,28 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
 }
 
+// Clusters of 1 .. 8 thread blocks (one per SM) that a B200 holds at a time.
+constexpr int kClusters[kMaxSplits] = {148, 74, 45, 33, 26, 22, 15, 15};
+
 template <int NP>
 cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   using Cfg = StreamCfg<NP>;
   StreamParams p;
   p.n = a.n;
   p.m = a.m;
-  p.n_blocks = (a.n + NP - 1) / NP;
+  p.tiles = (a.m + kTileM - 1) / kTileM;
   p.k_blocks = (a.k + kBlock - 1) / kBlock;
   p.units = (p.k_blocks + kUnit - 1) / kUnit;
-  const long long tiles = static_cast<long long>((a.m + kTileM - 1) / kTileM) * p.n_blocks;
-  if (tiles * p.units > INT32_MAX / 2) return cudaErrorInvalidValue;  // over 17 TB of weights
-  p.total = static_cast<int>(tiles) * p.units;
-  const int max_grid = std::min(num_sms, kMaxGrid);
-  int grid = std::min(max_grid, p.total);
-  // Few tiles: every range is a part of one tile (a range over two tiles leaves two partial sums, the first of them
-  // in the middle of its work).  More parts shorten the K loop (~0.55 us a unit) and lengthen the sum that the last
-  // one to arrive takes over all of them (~12 ns a part and token): the number of parts balances the two.
-  p.splits = 0;
-  if (tiles * 2 <= max_grid) {
-    const int most = std::min(max_grid / static_cast<int>(tiles), p.units);
-    float best = 0.f;
-    for (int parts = 1; parts <= most; ++parts) {
-      const float us = 0.55f * static_cast<float>((p.units + parts - 1) / parts) +
-                       (parts > 1 ? 1.5f + 0.012f * static_cast<float>(parts * NP) : 0.f);
-      if (parts == 1 || us < best) {
-        best = us;
-        p.splits = parts;
-      }
-    }
-    grid = static_cast<int>(tiles) * p.splits;
-  }
-  p.base = p.total / grid;
-  p.more = p.total % grid;
+  // The split of K that leaves the fewest units to a thread block, among those whose clusters all run at once.
+  p.splits = 1;
+  for (int splits = 2; splits <= kMaxSplits && splits <= p.units; ++splits)
+    if (p.tiles <= kClusters[splits - 1] &&
+        (p.units + splits - 1) / splits < (p.units + p.splits - 1) / p.splits)
+      p.splits = splits;
   p.x_scale = a.x_scale;
   p.w_scale = a.w_scale;
   p.out_f32 = a.out_f32;
   p.out_bf16 = a.out_bf16;
-  p.part = host::at<float>(a.ws, kPartOff);
-  p.counters = host::at<int>(a.ws, kCounterOff);
   p.status = a.status;
   p.w_static = a.w_static;
   CUtensorMap wmap, xmap;
@@ -535,8 +468,21 @@ cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   e = cudaFuncSetAttribute(gemm_fp8_stream_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(Cfg::kSmem));
   if (e != cudaSuccess) return e;
-  return host::launch_pdl(gemm_fp8_stream_kernel<NP>, dim3(static_cast<unsigned>(grid)), dim3(kStreamThreads),
-                          Cfg::kSmem, s, wmap, xmap, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.splits > 1 ? p.tiles * p.splits : std::min(num_sms, p.tiles)));
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_fp8_stream_kernel<NP>, wmap, xmap, p);
 }
 
 // ---------------------------------------------------------------- tiled product (many tokens)
