@@ -88,7 +88,6 @@ constexpr int kWBytes = kTileM * kBlock;        // one K block of a weight tile:
 constexpr int kUnit = 2;                        // K blocks per ring stage
 constexpr int kChunk = 16;                      // K blocks per scale slot
 constexpr int kStreamThreads = 256;             // warps: TMA, MMA, 2 of scales, 4 of accumulation
-constexpr int kAccBufs = 4;
 constexpr int kMaxSplits = 8;                   // thread blocks of a cluster
 
 template <int NP>
@@ -97,6 +96,7 @@ struct StreamCfg {
   static constexpr int kStageBytes = kUnit * (kWBytes + kXBytes);
   static constexpr int kStages = NP <= 32 ? 5 : NP == 64 ? 4 : 3;
   static constexpr int kScaleBytes = 2 * kChunk * NP * 4;
+  static constexpr int kAccBufs = NP <= 64 ? 4 : 2;  // accumulators of one unit: kUnit x NP columns
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 4 + 1;
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kScaleBytes + kNumBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     gemm_fp8_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                            StreamParams p) {
   using Cfg = StreamCfg<NP>;
+  constexpr int kAccBufs = Cfg::kAccBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem);
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     prefetch_tmap(&wmap);
     prefetch_tmap(&xmap);
   }
-  constexpr uint32_t kTmemCols = kAccBufs * NP;  // 64 .. 512
+  constexpr uint32_t kTmemCols = kAccBufs * kUnit * NP;  // 128 .. 512
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -256,30 +257,30 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     bool ok = true;
     for (int t = first; t < p.tiles && ok; t += step) {
       for (int u = u0; u < u1 && ok; ++u) {
-        ok = __all_sync(kAll, mbar_wait(full(st), ph, abort_flag));
+        ok = __all_sync(kAll, mbar_wait(full(st), ph, abort_flag) && mbar_wait(accempty(buf), aph ^ 1u, abort_flag));
         if (!ok) break;
         const int nkb = min(kUnit, p.k_blocks - kUnit * u);
         const uint32_t a = ring + st * Cfg::kStageBytes;
-        for (int h = 0; h < nkb; ++h) {
-          ok = __all_sync(kAll, mbar_wait(accempty(buf), aph ^ 1u, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // 32 K elements (bytes) per MMA
-              mma_e4m3(acc + buf * NP, sdesc_sw128(a + h * kWBytes + kk * 32, 16, 1024),
-                       sdesc_sw128(a + kUnit * kWBytes + h * Cfg::kXBytes + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-            mma_commit(accfull(buf));
+          for (int h = 0; h < kUnit; ++h) {
+            if (h < nkb) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)  // 32 K elements (bytes) per MMA
+                mma_e4m3(acc + (buf * kUnit + h) * NP, sdesc_sw128(a + h * kWBytes + kk * 32, 16, 1024),
+                         sdesc_sw128(a + kUnit * kWBytes + h * Cfg::kXBytes + kk * 32, 16, 1024), idesc,
+                         kk > 0 ? 1u : 0u);
+            }
           }
-          __syncwarp();
-          if (++buf == kAccBufs) {
-            buf = 0;
-            aph ^= 1u;
-          }
+          mma_commit(accfull(buf));
+          mma_commit(empty(st));
         }
-        if (!ok) break;
-        if (elect_one()) mma_commit(empty(st));
         __syncwarp();
+        if (++buf == kAccBufs) {
+          buf = 0;
+          aph ^= 1u;
+        }
         if (++st == Cfg::kStages) {
           st = 0;
           ph ^= 1u;
@@ -349,27 +350,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (!ok) break;
         const float* sc = scales + slot * kChunk * NP;
         const int kb1 = min(kb0 + kChunk, kb_end);
-        for (int kb = kb0; kb < kb1; ++kb, sc += NP) {
+        for (int kb = kb0; kb < kb1; kb += kUnit, sc += kUnit * NP) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(accfull(buf), aph, abort_flag));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t src = tmem + lane_addr + buf * NP;
-          constexpr int kCols = NP < 32 ? NP : 32;
+          const uint32_t src = tmem + lane_addr + buf * kUnit * NP;
+          // up to 64 columns a load (a whole unit of 16 or 32 tokens); columns past the last K block go unused
+          constexpr int kCols = kUnit * NP < 64 ? kUnit * NP : 64;
 #pragma unroll
-          for (int c = 0; c < NP; c += kCols) {
+          for (int c = 0; c < kUnit * NP; c += kCols) {
+            if (c >= NP && kb + 1 >= kb1) break;
             float v[kCols];
-            if constexpr (kCols == 16) {
-              tmem_ld16(src + c, v);
-            } else {
+            if constexpr (kCols == 32) {
               tmem_ld32(src + c, v);
+            } else {
+              tmem_ld64(src + c, v);
             }
 #pragma unroll
             for (int i = 0; i < kCols; i += 4) {
+              const int j = (c + i) % NP;
+              if (i == NP && kb + 1 >= kb1) break;
               const float4 s4 = *reinterpret_cast<const float4*>(sc + c + i);
-              acc[c + i] = fmaf(v[i], s4.x, acc[c + i]);
-              acc[c + i + 1] = fmaf(v[i + 1], s4.y, acc[c + i + 1]);
-              acc[c + i + 2] = fmaf(v[i + 2], s4.z, acc[c + i + 2]);
-              acc[c + i + 3] = fmaf(v[i + 3], s4.w, acc[c + i + 3]);
+              acc[j] = fmaf(v[i], s4.x, acc[j]);
+              acc[j + 1] = fmaf(v[i + 1], s4.y, acc[j + 1]);
+              acc[j + 2] = fmaf(v[i + 2], s4.z, acc[j + 2]);
+              acc[j + 3] = fmaf(v[i + 3], s4.w, acc[j + 3]);
             }
           }
           tc_fence_before();
