@@ -87,7 +87,6 @@ constexpr int kTileM = 128;                     // weight rows per tile
 constexpr int kWBytes = kTileM * kBlock;        // one K block of a weight tile: 16 KB
 constexpr int kUnit = 2;                        // K blocks per ring stage
 constexpr int kChunk = 16;                      // K blocks per scale slot
-constexpr int kStreamThreads = 256;             // warps: TMA, MMA, 2 of scales, 4 of accumulation
 constexpr int kMaxSplits = 8;                   // thread blocks of a cluster
 
 template <int NP>
@@ -97,6 +96,11 @@ struct StreamCfg {
   static constexpr int kStages = NP <= 32 ? 5 : NP == 64 ? 4 : 3;
   static constexpr int kScaleBytes = 2 * kChunk * NP * 4;
   static constexpr int kAccBufs = NP <= 64 ? 4 : 2;  // accumulators of one unit: kUnit x NP columns
+  // Warps: TMA, MMA, 2 of scales, then 4 or 8 of accumulation; of 8, four take each half of the tokens (an
+  // accumulating warp's step is mostly the latency of its waits and loads, which the halves overlap).
+  static constexpr int kGroups = NP >= 32 ? 2 : 1;
+  static constexpr int kCols = NP / kGroups;
+  static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 4 + 1;
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kScaleBytes + kNumBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -125,7 +129,7 @@ __device__ __forceinline__ void store_y(const StreamParams& p, int row, int toke
 }
 
 template <int NP>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+__global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     gemm_fp8_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                            StreamParams p) {
   using Cfg = StreamCfg<NP>;
@@ -160,11 +164,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
     for (int a = 0; a < kAccBufs; ++a) {
       mbar_init(accfull(a), 1);
-      mbar_init(accempty(a), 4);  // one arrival per accumulating warp
+      mbar_init(accempty(a), 4 * Cfg::kGroups);  // one arrival per accumulating warp
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(sfull(a), 64);
-      mbar_init(sempty(a), 4);
+      mbar_init(sempty(a), 4 * Cfg::kGroups);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -334,47 +338,56 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else {
     // ------------------------------------------------------------ scaled accumulation
     // Warp w reads TMEM lane quarter w % 4: this thread's weight row is 32 (w % 4) + lane of the tile, its
-    // accumulators are the NP tokens.
-    const int quarter = warp & 3;
-    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    // accumulators are the tokens col0 .. col0 + kCols - 1.
+    constexpr int kCols = Cfg::kCols;
+    const int quarter = warp & 3, col0 = ((warp - 4) >> 2) * kCols;
+    const uint32_t src0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
     const int mrow = quarter * 32 + lane;
     int buf = 0, slot = 0;
     uint32_t aph = 0, sph = 0;
     bool ok = true;
-    float acc[NP];
+    float acc[kCols];
+    const auto add = [&](const float* v, const float* sc) {
+#pragma unroll
+      for (int i = 0; i < kCols; i += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sc + i);
+        acc[i] = fmaf(v[i], s4.x, acc[i]);
+        acc[i + 1] = fmaf(v[i + 1], s4.y, acc[i + 1]);
+        acc[i + 2] = fmaf(v[i + 2], s4.z, acc[i + 2]);
+        acc[i + 3] = fmaf(v[i + 3], s4.w, acc[i + 3]);
+      }
+    };
     for (int t = first; t < p.tiles && ok; t += step) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) acc[i] = 0.f;
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
       for (int kb0 = kUnit * u0; kb0 < kb_end && ok; kb0 += kChunk) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(sfull(slot), sph, abort_flag));
         if (!ok) break;
-        const float* sc = scales + slot * kChunk * NP;
+        const float* sc = scales + slot * kChunk * NP + col0;
         const int kb1 = min(kb0 + kChunk, kb_end);
         for (int kb = kb0; kb < kb1; kb += kUnit, sc += kUnit * NP) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(accfull(buf), aph, abort_flag));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t src = tmem + lane_addr + buf * kUnit * NP;
-          // up to 64 columns a load (a whole unit of 16 or 32 tokens); columns past the last K block go unused
-          constexpr int kCols = kUnit * NP < 64 ? kUnit * NP : 64;
-#pragma unroll
-          for (int c = 0; c < kUnit * NP; c += kCols) {
-            if (c >= NP && kb + 1 >= kb1) break;
-            float v[kCols];
-            if constexpr (kCols == 32) {
-              tmem_ld32(src + c, v);
+          // both K blocks of the unit (the second one's columns go unused past the last K block)
+          const uint32_t src = src0 + buf * kUnit * NP;
+          const bool two = kb + 1 < kb1;
+          if constexpr (kCols <= 32) {
+            float v[2 * kCols];
+            if constexpr (kCols == 16) {
+              tmem_ld16x2(src, src + NP, v);
             } else {
-              tmem_ld64(src + c, v);
+              tmem_ld32x2(src, src + NP, v);
             }
-#pragma unroll
-            for (int i = 0; i < kCols; i += 4) {
-              const int j = (c + i) % NP;
-              if (i == NP && kb + 1 >= kb1) break;
-              const float4 s4 = *reinterpret_cast<const float4*>(sc + c + i);
-              acc[j] = fmaf(v[i], s4.x, acc[j]);
-              acc[j + 1] = fmaf(v[i + 1], s4.y, acc[j + 1]);
-              acc[j + 2] = fmaf(v[i + 2], s4.z, acc[j + 2]);
-              acc[j + 3] = fmaf(v[i + 3], s4.w, acc[j + 3]);
+            add(v, sc);
+            if (two) add(v + kCols, sc + NP);
+          } else {
+            float v[kCols];
+            tmem_ld64(src, v);
+            add(v, sc);
+            if (two) {
+              tmem_ld64(src + NP, v);
+              add(v, sc + NP);
             }
           }
           tc_fence_before();
@@ -393,8 +406,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const int row = t * kTileM + mrow;
       if (ok && p.splits == 1 && row < p.m) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          if (i < p.n) store_y(p, row, i, acc[i]);
+        for (int i = 0; i < kCols; ++i)
+          if (col0 + i < p.n) store_y(p, row, col0 + i, acc[i]);
       }
     }
     if (!ok && lane == 0) {
@@ -410,17 +423,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       for (int r = 0; r < kMaxSplits; ++r) {
         if (r >= p.splits) break;
         const int c0 = NP * r / p.splits, c1 = NP * (r + 1) / p.splits;
-        const uint32_t dst = map_to_rank(ring, r) + 4u * ((rank * (c1 - c0) - c0) * kTileM + mrow);
+        const uint32_t dst = map_to_rank(ring, r) + 4u * ((rank * (c1 - c0) - c0 + col0) * kTileM + mrow);
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          if (i >= c0 && i < c1) st_cluster(dst + 4u * i * kTileM, acc[i]);
+        for (int i = 0; i < kCols; ++i)
+          if (col0 + i >= c0 && col0 + i < c1) st_cluster(dst + 4u * i * kTileM, acc[i]);
       }
       cluster_barrier();
       const int c0 = NP * rank / p.splits, c1 = NP * (rank + 1) / p.splits;
       const int row = first * kTileM + mrow;
       const float* part = reinterpret_cast<const float*>(smem) + mrow;
       if (ok && row < p.m) {
-        for (int i = c0; i < c1 && i < p.n; ++i) {
+        for (int i = c0 + (warp - 4) / 4; i < c1 && i < p.n; i += Cfg::kGroups) {
           float sum = 0.f;
           for (int r = 0; r < p.splits; ++r) sum += part[(r * (c1 - c0) + i - c0) * kTileM];
           store_y(p, row, i, sum);
@@ -475,7 +488,7 @@ cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.splits > 1 ? p.tiles * p.splits : std::min(num_sms, p.tiles)));
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3(Cfg::kThreads);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
