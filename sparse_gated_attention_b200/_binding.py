@@ -9,6 +9,7 @@ sm_100 GPU the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -163,14 +164,19 @@ def _need(t, name, dtype, shape=None):
     return t
 
 
-def _empty(shape, dtype, device):
-    """A contiguous tensor: torch.empty at half its cost, which counts in a decode step's short calls."""
+@functools.lru_cache(maxsize=1024)
+def _strides(shape) -> tuple:
+    """The strides of a contiguous tensor."""
     strides, n = [], 1
     for d in reversed(shape):
         strides.append(n)
         n *= d
-    strides.reverse()
-    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    return tuple(reversed(strides))
+
+
+def _empty(shape, dtype, device):
+    """A contiguous tensor: torch.empty at half its cost, which counts in a decode step's short calls."""
+    return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
 
 
 def _one_device(*tensors):
@@ -181,9 +187,9 @@ def _one_device(*tensors):
             raise ValueError(f"expected every tensor on the current device cuda:{dev}, got one on {t.device}")
 
 
-def _need_fp8(t, name, shape):
+def _need_fp8(t, name, shape=None):
     """An E4M3 tensor: torch.float8_e4m3fn, or its bytes as uint8."""
-    if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn:
         return _need(t, name, torch.float8_e4m3fn, shape)  # the library takes its address: no view is needed
     return _need(t, name, torch.uint8, shape)
 
@@ -369,23 +375,26 @@ def forward_fused_fp8(q_idx, w, k_idx, q, kv, gate, q_pos, top_k: int = TOP_K, i
 
 
 # ----------------------------------------------------------------------------- the latent cache in 4 bits
-def _status_ws(ws, device):
-    return torch.zeros(STATUS_BYTES, dtype=torch.uint8, device=device) if ws is None else ws
+def _status_ws(device):
+    return torch.zeros(STATUS_BYTES, dtype=torch.uint8, device=device)
 
 
 def kv4_append(kv_rows, q_pos, kv4, ws=None, stream=None):
     """Quantises kv_rows [B,T,576] bf16 into the 4-bit cache kv4 [B,L,416] uint8 at q_pos [B,T]
     (sga_kv4_append); returns kv4, written in place."""
-    B, T = kv_rows.shape[0], kv_rows.shape[1]
+    B, T = q_pos.shape
     L = kv4.shape[1]
     _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
-    _need(q_pos, "q_pos", torch.int32, (B, T))
+    _need(q_pos, "q_pos", torch.int32)
     _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
-    dims = make_dims(B, T, L)
-    ws = _status_ws(ws, kv4.device)
+    if ws is None:
+        ws = _status_ws(kv4.device)
     _one_device(kv_rows, q_pos, kv4, ws)
-    _check("sga_kv4_append", load_library().sga_kv4_append(
-        ctypes.byref(dims), _ptr(kv_rows), _ptr(q_pos), _ptr(kv4), _ptr(ws), ws.numel(), _stream(stream)))
+    st = (_lib or load_library()).sga_kv4_append(
+        Dims(B, T, L, TOP_K), kv_rows.data_ptr(), q_pos.data_ptr(), kv4.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(stream))
+    if st:
+        raise SGAError("sga_kv4_append", st)
     return kv4
 
 
@@ -394,39 +403,43 @@ def kv4_read(kv4, pos, kv_rows=None, ws=None, stream=None):
     B, T = pos.shape
     L = kv4.shape[1]
     _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
-    _need(pos, "pos", torch.int32, (B, T))
+    _need(pos, "pos", torch.int32)
     if kv_rows is None:
         kv_rows = _empty((B, T, QK_DIM), torch.bfloat16, kv4.device)
     else:
         _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
-    dims = make_dims(B, T, L)
-    ws = _status_ws(ws, kv4.device)
+    if ws is None:
+        ws = _status_ws(kv4.device)
     _one_device(kv4, pos, kv_rows, ws)
-    _check("sga_kv4_read", load_library().sga_kv4_read(
-        ctypes.byref(dims), _ptr(kv4), _ptr(pos), _ptr(kv_rows), _ptr(ws), ws.numel(), _stream(stream)))
+    st = (_lib or load_library()).sga_kv4_read(
+        Dims(B, T, L, TOP_K), kv4.data_ptr(), pos.data_ptr(), kv_rows.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(stream))
+    if st:
+        raise SGAError("sga_kv4_read", st)
     return kv_rows
 
 
 def sparse_mla_attend_kv4(q, kv4, idx, gate=None, out=None, ws=None, stream=None):
     """Sparse latent attention over the 4-bit cache + sigmoid head gate -> out [B,T,64,512] bf16."""
-    B, T = q.shape[0], q.shape[1]
+    B, T, K = idx.shape
     L = kv4.shape[1]
-    K = idx.shape[-1]
     _need(q, "q", torch.bfloat16, (B, T, HEADS, QK_DIM))
     _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
-    _need(idx, "idx", torch.int32, (B, T, K))
+    _need(idx, "idx", torch.int32)
     if gate is not None:
         _need(gate, "gate", torch.bfloat16, (B, T, HEADS))
-    dims = make_dims(B, T, L, K)
     if out is None:
         out = _empty((B, T, HEADS, V_DIM), torch.bfloat16, q.device)
     else:
         _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
-    ws = _status_ws(ws, q.device)
+    if ws is None:
+        ws = _status_ws(q.device)
     _one_device(q, kv4, idx, gate, out, ws)
-    _check("sga_sparse_mla_attend_kv4", load_library().sga_sparse_mla_attend_kv4(
-        ctypes.byref(dims), _ptr(q), _ptr(kv4), _ptr(idx), _ptr(gate), _ptr(out), _ptr(ws), ws.numel(),
-        _stream(stream)))
+    st = (_lib or load_library()).sga_sparse_mla_attend_kv4(
+        Dims(B, T, L, K), q.data_ptr(), kv4.data_ptr(), idx.data_ptr(), _ptr(gate), out.data_ptr(), ws.data_ptr(),
+        ws.numel(), _stream(stream))
+    if st:
+        raise SGAError("sga_sparse_mla_attend_kv4", st)
     return out
 
 
@@ -480,9 +493,27 @@ def quantize_fp8(x, codes=None, scale=None, stream=None):
     else:
         _need(scale, "scale", torch.float32, s_shape)
     _one_device(x, codes, scale)
-    _check("sga_quantize_fp8", load_library().sga_quantize_fp8(
-        n // K, K, _ptr(x), _ptr(codes), _ptr(scale), _stream(stream)))
+    st = (_lib or load_library()).sga_quantize_fp8(
+        n // K, K, x.data_ptr(), codes.data_ptr(), scale.data_ptr(), _stream(stream))
+    if st:
+        raise SGAError("sga_quantize_fp8", st)
     return codes, scale
+
+
+@functools.lru_cache(maxsize=1024)
+def _gemm_fp8_shapes(x_shape, w_shape):
+    """Tokens, and the shapes of x_scale, w_scale and the output of gemm_fp8."""
+    if len(w_shape) != 2 or len(x_shape) < 1 or x_shape[-1] != w_shape[1]:
+        raise ValueError(f"x: expected [..., K] and w: [M, K], got {tuple(x_shape)} and {tuple(w_shape)}")
+    M, K = w_shape
+    lead = tuple(x_shape[:-1])
+    n = 1
+    for d in lead:
+        n *= d
+    if n == 0 or M == 0 or K == 0:
+        raise ValueError("x, w: must have at least one element")
+    kb = -(-K // FP8_BLOCK)
+    return n, (*lead, kb), (-(-M // FP8_BLOCK), kb), (*lead, M)
 
 
 def alloc_gemm_fp8_workspace(device=None) -> torch.Tensor:
@@ -493,33 +524,30 @@ def alloc_gemm_fp8_workspace(device=None) -> torch.Tensor:
 def gemm_fp8(x, x_scale, w, w_scale, out_dtype=torch.float32, out=None, ws=None, stream=None):
     """The product x w^T of E4M3 activations x [..., K] and weights w [M, K] with the scales x_scale
     [..., ceil(K / 128)] and w_scale [ceil(M / 128), ceil(K / 128)] fp32 (sga_gemm_fp8) -> [..., M], fp32 or bf16."""
-    if not isinstance(w, torch.Tensor) or w.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() < 1:
-        raise ValueError("x: expected [..., K] and w: [M, K]")
-    M, K = w.shape
-    lead = x.shape[:-1]
-    kb = -(-K // FP8_BLOCK)
-    _need_fp8(x, "x", (*lead, K))
-    _need_fp8(w, "w", (M, K))
-    _need(x_scale, "x_scale", torch.float32, (*lead, kb))
-    _need(w_scale, "w_scale", torch.float32, (-(-M // FP8_BLOCK), kb))
-    n = x.numel()
-    if n == 0 or M == 0:
-        raise ValueError("x, w: must have at least one element")
-    if out is None:
-        if out_dtype not in _OUT_TYPES:
-            raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
-        out = _empty((*lead, M), out_dtype, x.device)
-    else:
+    w_shape = w.shape
+    n, xs_shape, ws_shape, y_shape = _gemm_fp8_shapes(x.shape, w_shape)
+    M, K = w_shape
+    _need_fp8(x, "x")
+    _need_fp8(w, "w")
+    _need(x_scale, "x_scale", torch.float32, xs_shape)
+    _need(w_scale, "w_scale", torch.float32, ws_shape)
+    if out is not None:
         out_dtype = out.dtype
-        if out_dtype not in _OUT_TYPES:
-            raise TypeError(f"out: expected torch.float32 or torch.bfloat16, got {out_dtype}")
-        _need(out, "out", out_dtype, (*lead, M))
+    kind = _OUT_TYPES.get(out_dtype)
+    if kind is None:
+        raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
+    if out is None:
+        out = _empty(y_shape, out_dtype, x.device)
+    else:
+        _need(out, "out", out_dtype, y_shape)
     if ws is None:
         ws = alloc_gemm_fp8_workspace(x.device)
     _one_device(x, x_scale, w, w_scale, out, ws)
-    _check("sga_gemm_fp8", load_library().sga_gemm_fp8(
-        n // K, M, K, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(out), _OUT_TYPES[out_dtype], _ptr(ws),
-        ws.numel(), _stream(stream)))
+    st = (_lib or load_library()).sga_gemm_fp8(
+        n, M, K, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), kind,
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        raise SGAError("sga_gemm_fp8", st)
     return out
 
 
