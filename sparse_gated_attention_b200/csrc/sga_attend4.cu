@@ -7,8 +7,8 @@
 //
 // What differs from the bf16 kernel follows from the row being 2.8 times smaller:
 //   * A chunk's 64 rows are 26 KB, so they are gathered into registers: eight
-//     producer warps hold the next chunk's codes while they store the current
-//     one's expanded tiles, and the whole value ring in shared memory is left to expanded tiles.
+//     producer warps hold the next two chunks' codes while they expand and store
+//     the current one, and the whole value ring in shared memory is left to expanded tiles.
 //   * A code times its scale has at most 6 significant bits between 2^-10 and
 //     2,688, so it is exact in fp16 (and in bf16).  The tiles hold fp16: two
 //     codes expand with one conversion and one multiplication, and P can be one
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     const int r = ptid >> 2;    // this thread's row of the chunk
     const int part = ptid & 3;  // and its quarter of that row
     bool ok = true;
-    // Indices are fetched two chunks ahead and looked at only when the rows are loaded, one chunk ahead (into the
-    // registers that the chunk's expansion has just left).
+    // Rows are loaded two chunks ahead, at the end of an iteration, so that they have a whole one to arrive; their
+    // indices are fetched one iteration before that.
     auto load_idx = [&](int j) {
       // K is a multiple of 64: a chunk has no tail
       return j < nchunks ? __ldg(idx_row + slot_base + j * kChunk + r) : -1;
@@ -277,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       load_row(d, kv_b + static_cast<size_t>(valid ? v : 0) * kRowBytes, part, valid);
       return valid;
     };
-    const int first_idx = load_idx(0);
-    int ahead_idx = load_idx(1);
-    RowPart cur;
-    bool cur_valid;
+    const int first_idx = load_idx(0), second_idx = load_idx(1);
+    int ahead_idx = load_idx(2);
+    RowPart cur, next;
+    bool cur_valid, next_valid = false;
     {
       // Q: four threads per head, 16-byte pieces part, part + 4, ...; pieces 64.. are the rope dims
       const int h = r;
@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
+    if (nchunks > 1) next_valid = load(next, second_idx);
     // This thread's 32 dims of a pair are four 16-byte columns of box part / 2.  The upper box's threads take their
     // words in the order 2, 3, 0, 1, so the eight threads of a store phase reach eight different columns.
     const uint32_t flip = part & 2;
@@ -327,36 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
 #pragma unroll
     for (int i = 0; i < 4; ++i) col[i] = ((((part & 1) * 4) + (i ^ flip)) ^ (r & 7)) << 4;
     for (int j = 0; j < nchunks; ++j) {
-      // The chunk is expanded in registers before its slots are free, so that only the stores stand between PV(j - 2)
-      // and QK^T(j).
-      uint4 tile[kPairsPerChunk][4];
-#pragma unroll
-      for (int q = 0; q < kPairsPerChunk; ++q) {
-        // the scales of pair q are with thread q of the row's four; this thread's two are its half word `part`
-        const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, cur.scales.x, (lane & ~3) + q);
-        const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, cur.scales.y, (lane & ~3) + q);
-        const uint32_t two = ((part & 2) ? w1 : w0) >> (16 * (part & 1));
-        uint32_t s0, s1;
-        expand_scales(two & 0xFFFFu, s0, s1);
-        const uint4 c = cur.codes[q];
-        const uint32_t sa = flip ? s1 : s0, sb = flip ? s0 : s1;
-        tile[q][0] = expand_codes(flip ? c.z : c.x, sa);
-        tile[q][1] = expand_codes(flip ? c.w : c.y, sa);
-        tile[q][2] = expand_codes(flip ? c.x : c.z, sb);
-        tile[q][3] = expand_codes(flip ? c.y : c.w, sb);
-      }
       const uint32_t seen = __ballot_sync(0xFFFFFFFFu, cur_valid);
       const int rs = j % kRopeRing;
-      ok = mbar_wait(rope_empty(rs), static_cast<uint32_t>((j / kRopeRing) & 1) ^ 1u, abort_flag);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(rope_empty(rs), static_cast<uint32_t>((j / kRopeRing) & 1) ^ 1u, abort_flag));
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         st_shared16(rope + rs * kBoxBytes + r * 128 + (((2 * part + i) ^ (r & 7)) << 4), cur.rope[i]);
-      if (j + 1 < nchunks) {
-        cur_valid = load(cur, ahead_idx);
-        ahead_idx = load_idx(j + 2);
-      }
       __syncwarp();
       if (lane == 0) {
         // Validity of the warp's eight rows (every fourth ballot bit) -> bits 8 warp .. of the chunk's mask, which
@@ -369,20 +347,48 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         reinterpret_cast<uint8_t*>(masks + j % kMaskRing)[warp] = static_cast<uint8_t>(m);
         mbar_arrive(rope_full(rs));
       }
-      // value dims 128 q .. 128 q + 127 -> pair slot (4 j + q) mod 8
+      // Value dims 128 q .. 128 q + 127 -> pair slot (4 j + q) mod 8, two pairs at a time: the first two are expanded in
+      // registers before their slots are free, the other two while QK^T reads the first.
 #pragma unroll
-      for (int q = 0; q < kPairsPerChunk; ++q) {
-        const int n = j * kPairsPerChunk + q;
-        const int slot = n % kPairRing;
-        ok = mbar_wait(pair_empty(slot), static_cast<uint32_t>((n / kPairRing) & 1) ^ 1u, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+      for (int half = 0; half < 2; ++half) {
+        uint4 tile[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st_shared16(dst0 + slot * kPairBytes + col[i], tile[q][i]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pair_full(slot));
+        for (int i = 0; i < 2; ++i) {
+          const int q = 2 * half + i;
+          // the scales of pair q are with thread q of the row's four; this thread's two are its half word `part`
+          const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, cur.scales.x, (lane & ~3) + q);
+          const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, cur.scales.y, (lane & ~3) + q);
+          const uint32_t two = ((part & 2) ? w1 : w0) >> (16 * (part & 1));
+          uint32_t s0, s1;
+          expand_scales(two & 0xFFFFu, s0, s1);
+          const uint4 c = cur.codes[q];
+          const uint32_t sa = flip ? s1 : s0, sb = flip ? s0 : s1;
+          tile[i][0] = expand_codes(flip ? c.z : c.x, sa);
+          tile[i][1] = expand_codes(flip ? c.w : c.y, sa);
+          tile[i][2] = expand_codes(flip ? c.x : c.z, sb);
+          tile[i][3] = expand_codes(flip ? c.y : c.w, sb);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = j * kPairsPerChunk + 2 * half + i;
+          const int slot = n % kPairRing;
+          ok = ok && mbar_wait(pair_empty(slot), static_cast<uint32_t>((n / kPairRing) & 1) ^ 1u, abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (ok) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared16(dst0 + slot * kPairBytes + col[k], tile[i][k]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pair_full(slot));
+          }
+        }
       }
       if (!ok) break;
+      cur = next;
+      cur_valid = next_valid;
+      if (j + 2 < nchunks) {
+        next_valid = load(next, ahead_idx);
+        ahead_idx = load_idx(j + 3);
+      }
     }
     if (!ok) {
       record_status(p.status, kStatusTimeout);
@@ -541,10 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
             ps[2 * (k & 1) + e] += x;
           }
         }
-        float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
-        psum += __shfl_xor_sync(0xFFFFFFFFu, psum, 1);
-        psum += __shfl_xor_sync(0xFFFFFFFFu, psum, 2);
-        l_run[i] = l_run[i] * alpha[i] + psum;
+        l_run[i] = l_run[i] * alpha[i] + ((ps[0] + ps[1]) + (ps[2] + ps[3]));  // this thread's columns
       }
       // PV_{j-1} must be done before P and O are touched.
       ok = ok && mbar_wait(p_free, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag);
@@ -582,6 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     if (!ok) {
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l_run[i] += __shfl_xor_sync(0xFFFFFFFFu, l_run[i], 1);
+      l_run[i] += __shfl_xor_sync(0xFFFFFFFFu, l_run[i], 2);
     }
     if (m4 == 0) {
       own_ml[hrow[0]] = make_float2(m_ref[0], l_run[0]);
@@ -648,10 +656,16 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         float o[32];
         tmem_ld32(tmem + lane_addr + blk * kHeads + c * 32, o);
         if (S == 1) {
-          uint16_t* col = p.out + static_cast<size_t>(row) * kHeads * kDv + static_cast<size_t>(c * 32) * kDv + dim;
+          // neighbouring lanes trade a head: the even one stores both dims of head i, the odd one of head i + 1
+          uint16_t* col = p.out + static_cast<size_t>(row) * kHeads * kDv +
+                          static_cast<size_t>(c * 32 + (lane & 1)) * kDv + (dim & ~1);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            col[static_cast<size_t>(i) * kDv] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * hf[i]));
+          for (int i = 0; i < 32; i += 2) {
+            const float a = o[i] * hf[i], b = o[i + 1] * hf[i + 1];
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : b, 1);
+            *reinterpret_cast<uint32_t*>(col + static_cast<size_t>(i) * kDv) =
+                lane & 1 ? pack_bf16(got, b) : pack_bf16(a, got);
+          }
         } else {
           const int v = dim >> 2;
           const int owner = ((v + 1) * S - 1) / (kDv / 4);  // the r with v0(r) <= v < v0(r + 1)
