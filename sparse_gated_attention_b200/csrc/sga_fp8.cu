@@ -138,8 +138,8 @@ struct StreamCfg {
 };
 
 struct StreamParams {
-  int n, m, tiles, k_blocks, units;  // units: pairs of K blocks in a tile
-  int splits;                        // thread blocks (a cluster) that share a tile's K
+  int n, m, n_blocks, tiles, k_blocks, units;  // tiles: 128 weight rows x NP tokens; units: pairs of K blocks in one
+  int splits;                                  // thread blocks (a cluster) that share a tile's K
   const float* x_scale;
   const float* w_scale;
   float* out_f32;
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
-  // This thread block's tiles (weight rows 128 t ..) and its part [u0, u1) of each one's K.
+  // This thread block's tiles (token blocks fastest, so that neighbours share weights) and its part [u0, u1) of each
+  // one's K.
   const int rank = blockIdx.x % p.splits;
   const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
   const int u0 = p.units * rank / p.splits, u1 = p.units * (rank + 1) / p.splits;
@@ -222,17 +223,17 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+      const uint64_t pol_w = p.n_blocks == 1 ? policy_evict_first() : policy_evict_last(), pol_x = policy_evict_last();
       const auto blocks_of = [&](int u) { return min(kUnit, p.k_blocks - kUnit * u); };
-      auto load_w = [&](int st, int t, int u) {
+      auto load_w = [&](int st, int row0, int u) {
         const uint32_t dst = ring + st * Cfg::kStageBytes;
         for (int h = 0; h < blocks_of(u); ++h)
-          tma_load_2d(dst + h * kWBytes, &wmap, full(st), (kUnit * u + h) * kBlock, t * kTileM, pol_w);
+          tma_load_2d(dst + h * kWBytes, &wmap, full(st), (kUnit * u + h) * kBlock, row0, pol_w);
       };
-      auto load_x = [&](int st, int u) {
+      auto load_x = [&](int st, int token0, int u) {
         const uint32_t dst = ring + st * Cfg::kStageBytes + kUnit * kWBytes;
         for (int h = 0; h < blocks_of(u); ++h)
-          tma_load_2d(dst + h * Cfg::kXBytes, &xmap, full(st), (kUnit * u + h) * kBlock, 0, pol_x);
+          tma_load_2d(dst + h * Cfg::kXBytes, &xmap, full(st), (kUnit * u + h) * kBlock, token0, pol_x);
       };
       // While the kernel before this one runs: weights that it cannot write are loaded into the first stages; others
       // are only brought into L2, which holds whatever it writes.
@@ -240,10 +241,10 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
       for (; pre < Cfg::kStages && u0 + pre < u1; ++pre) {
         if (p.w_static) {
           mbar_arrive_expect_tx(full(pre), blocks_of(u0 + pre) * (kWBytes + Cfg::kXBytes));
-          load_w(pre, first, u0 + pre);
+          load_w(pre, first / p.n_blocks * kTileM, u0 + pre);
         } else {
           for (int h = 0; h < blocks_of(u0 + pre); ++h)
-            tma_prefetch_2d(&wmap, (kUnit * (u0 + pre) + h) * kBlock, first * kTileM);
+            tma_prefetch_2d(&wmap, (kUnit * (u0 + pre) + h) * kBlock, first / p.n_blocks * kTileM);
         }
       }
       if (!p.w_static) pre = 0;
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
       long long issued = 0;
       bool ok = true;
       for (int t = first; t < p.tiles && ok; t += step) {
+        const int row0 = t / p.n_blocks * kTileM, token0 = t % p.n_blocks * NP;
         for (int u = u0; u < u1; ++u, ++n_done) {
           if (n_done >= pre) {
             if (!mbar_wait(empty(st), ph ^ 1u, abort_flag)) {
@@ -261,9 +263,9 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
               break;
             }
             mbar_arrive_expect_tx(full(st), blocks_of(u) * (kWBytes + Cfg::kXBytes));
-            load_w(st, t, u);
+            load_w(st, row0, u);
           }
-          load_x(st, u);
+          load_x(st, token0, u);
           ++issued;
           if (++st == Cfg::kStages) {
             st = 0;
@@ -337,7 +339,8 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     for (int t = first; t < p.tiles && ok; t += step) {
-      const float* ws = p.w_scale + static_cast<size_t>(t) * p.k_blocks;
+      const float* ws = p.w_scale + static_cast<size_t>(t / p.n_blocks) * p.k_blocks;
+      const int token0 = t % p.n_blocks * NP;
       for (int kb0 = kUnit * u0; kb0 < kb_end; kb0 += kChunk) {
         // this thread's K block and every fourth token, all loads before the first store (addresses past the end are
         // clamped: their products scale zeros or go unused)
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
         float v[NP / 4];
 #pragma unroll
         for (int i = 0; i < NP / 4; ++i)
-          v[i] = __ldg(p.x_scale + static_cast<size_t>(min(tok0 + 4 * i, p.n - 1)) * p.k_blocks + kb);
+          v[i] = __ldg(p.x_scale + static_cast<size_t>(min(token0 + tok0 + 4 * i, p.n - 1)) * p.k_blocks + kb);
         if (!mbar_wait(sempty(slot), ph ^ 1u, abort_flag)) {
           ok = false;
           break;
@@ -432,11 +435,11 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
         slot ^= 1;
         if (slot == 0) sph ^= 1u;
       }
-      const int row = t * kTileM + mrow;
+      const int row = t / p.n_blocks * kTileM + mrow, token0 = t % p.n_blocks * NP + col0;
       if (ok && p.splits == 1 && row < p.m) {
 #pragma unroll
         for (int i = 0; i < kCols; ++i)
-          if (col0 + i < p.n) store_y(p, row, col0 + i, acc[i]);
+          if (token0 + i < p.n) store_y(p, row, token0 + i, acc[i]);
       }
     }
     if (!ok && lane == 0) {
@@ -445,27 +448,30 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     }
     __syncwarp();
     if (p.splits > 1) {
-      // A tile shared by the cluster (its only one): thread block r sums tokens [NP r / S, NP (r + 1) / S) over the
-      // ranks in order.  Each sends its partial sums of those tokens to r, into the idle ring.
+      // A tile shared by the cluster (its only one): thread block r sums tokens c0(r) .. c0(r + 1) - 1, c0(r) = NP r / S,
+      // over the ranks in order.  Each sends its partial sums of those tokens to r, into the idle ring, as
+      // [source][token][128 rows].
+      const int S = p.splits, width = (NP + S - 1) / S;
+      const uint32_t inv = 65536u / S + 1;  // x / S = x * inv >> 16 for x <= 8 NP
+      const auto c0_of = [&](int r) { return static_cast<int>((static_cast<uint32_t>(NP * r) * inv) >> 16); };
       cluster_barrier();  // every MMA of the cluster has finished
+      const uint32_t mine = ring + 4u * (rank * width * kTileM + mrow);
 #pragma unroll
-      for (int r = 0; r < kMaxSplits; ++r) {
-        if (r >= p.splits) break;
-        const int c0 = NP * r / p.splits, c1 = NP * (r + 1) / p.splits;
-        const uint32_t dst = map_to_rank(ring, r) + 4u * ((rank * (c1 - c0) - c0 + col0) * kTileM + mrow);
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (col0 + i >= c0 && col0 + i < c1) st_cluster(dst + 4u * i * kTileM, acc[i]);
+      for (int i = 0; i < kCols; ++i) {
+        const int c = col0 + i, r = ((c + 1) * S - 1) / NP;  // the r with c0(r) <= c < c0(r + 1)
+        st_cluster(map_to_rank(mine + 4u * (c - c0_of(r)) * kTileM, r), acc[i]);
       }
       cluster_barrier();
-      const int c0 = NP * rank / p.splits, c1 = NP * (rank + 1) / p.splits;
-      const int row = first * kTileM + mrow;
+      const int c0 = c0_of(rank), c1 = c0_of(rank + 1);
+      const int row = first / p.n_blocks * kTileM + mrow, token0 = first % p.n_blocks * NP;
       const float* part = reinterpret_cast<const float*>(smem) + mrow;
       if (ok && row < p.m) {
-        for (int i = c0 + (warp - 4) / 4; i < c1 && i < p.n; i += Cfg::kGroups) {
+        const int last = min(c1, p.n - token0);
+#pragma unroll 4
+        for (int i = c0 + (warp - 4) / 4; i < last; i += Cfg::kGroups) {
           float sum = 0.f;
-          for (int r = 0; r < p.splits; ++r) sum += part[(r * (c1 - c0) + i - c0) * kTileM];
-          store_y(p, row, i, sum);
+          for (int r = 0; r < S; ++r) sum += part[(r * width + i - c0) * kTileM];
+          store_y(p, row, token0 + i, sum);
         }
       }
     }
@@ -486,21 +492,41 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
 // Clusters of 1 .. 8 thread blocks (one per SM) that a B200 holds at a time.
 constexpr int kClusters[kMaxSplits] = {148, 74, 45, 33, 26, 22, 15, 15};
 
+// What the kernel takes for `tiles` tiles of NP tokens, in microseconds, and the split of K it takes it with.  Fitted to
+// runs of 1 to 8 splits at 300 x 4096, 300 x 512, 2304 x 1536 and 1111 x 1552 weights with 8, 32, 64 and 96 tokens: a
+// unit 0.6 (16 tokens) to 0.9 us (128 tokens); a split's barriers 1 us and its exchange and sum 2.5 to 5 us shared out over
+// its thread blocks (two units in one thread block 3.5 us, in two 5.1; sixteen in one 12.0, in eight 4.7).  Only splits
+// whose clusters all run at once are considered.
+struct StreamPlan {
+  int splits;
+  float us;
+};
+StreamPlan stream_plan(int np, long long tiles, int units) {
+  const float unit = 0.57f + 0.0026f * np;
+  const float base = 1.7f + 0.035f * np;
+  StreamPlan best = {1, base + unit * static_cast<float>(units) * static_cast<float>((tiles + 147) / 148)};
+  for (int splits = 2; splits <= kMaxSplits && splits <= units; ++splits) {
+    if (tiles > kClusters[splits - 1]) break;
+    const float us = base + unit * static_cast<float>((units + splits - 1) / splits) + 1.f +
+                     (2.2f + 0.022f * np) / static_cast<float>(splits);
+    if (us < best.us) best = {splits, us};
+  }
+  return best;
+}
+
 template <int NP>
 cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   using Cfg = StreamCfg<NP>;
   StreamParams p;
   p.n = a.n;
   p.m = a.m;
-  p.tiles = (a.m + kTileM - 1) / kTileM;
+  p.n_blocks = (a.n + NP - 1) / NP;
+  const long long tiles = static_cast<long long>((a.m + kTileM - 1) / kTileM) * p.n_blocks;
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  p.tiles = static_cast<int>(tiles);
   p.k_blocks = (a.k + kBlock - 1) / kBlock;
   p.units = (p.k_blocks + kUnit - 1) / kUnit;
-  // The split of K that leaves the fewest units to a thread block, among those whose clusters all run at once.
-  p.splits = 1;
-  for (int splits = 2; splits <= kMaxSplits && splits <= p.units; ++splits)
-    if (p.tiles <= kClusters[splits - 1] &&
-        (p.units + splits - 1) / splits < (p.units + p.splits - 1) / p.splits)
-      p.splits = splits;
+  p.splits = stream_plan(NP, tiles, p.units).splits;
   p.x_scale = a.x_scale;
   p.w_scale = a.w_scale;
   p.out_f32 = a.out_f32;
@@ -920,7 +946,15 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   if (a.n <= 16) return launch_stream<16>(a, num_sms, s);
   if (a.n <= 32) return launch_stream<32>(a, num_sms, s);
   if (a.n <= 64) return launch_stream<64>(a, num_sms, s);
-  if (a.n <= 128) return launch_stream<128>(a, num_sms, s);
+  // More tokens: blocks of 128 through the streaming kernel, whose split K shortens a product of few tiles, or tiles of
+  // 256 x 256, each over the whole of K (0.5 us a K block), which read the operands less often.  256 tokens, m x k of
+  // 2304 x 7168: 19.6 us against 34.8; 400 tokens, 7168 x 8192: 64.2 against 40.3.
+  const long long k_blocks = (a.k + kBlock - 1) / kBlock;
+  const long long m128 = (a.m + kTileM - 1) / kTileM, n128 = (a.n + 127) / 128;
+  const long long waves = (((a.m + kTN - 1) / kTN) * static_cast<long long>((a.n + 2 * kTM - 1) / (2 * kTM)) + 73) / 74;
+  const float tile_us = 6.f + 0.5f * static_cast<float>(k_blocks * waves);
+  if (stream_plan(128, m128 * n128, static_cast<int>((k_blocks + kUnit - 1) / kUnit)).us < tile_us)
+    return launch_stream<128>(a, num_sms, s);
   return launch_tile(a, num_sms, s);
 }
 

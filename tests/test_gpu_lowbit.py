@@ -140,7 +140,9 @@ def check_product(n, m, k, out_dtype, seed=0, ws=None):
 
 PRODUCT_SHAPES = [(1, 1, 16), (1, 128, 128), (2, 129, 144), (16, 64, 4112), (17, 300, 272), (31, 2304, 7168),
                   (33, 1000, 1552), (64, 256, 512), (65, 130, 656), (127, 384, 1536), (129, 257, 400),
-                  (333, 1111, 1552), (512, 640, 2048), (1000, 300, 144)]
+                  (333, 1111, 1552), (512, 640, 2048), (1000, 300, 144),
+                  # tiles of 256 x 256: odd output rows, one wave and several, a short last tile each way
+                  (700, 2304, 272), (2000, 1111, 272), (400, 7168, 1024), (2300, 4000, 400)]
 
 
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
@@ -149,7 +151,8 @@ def test_product_matches_definition(n, m, k, out_dtype):
     check_product(n, m, k, out_dtype, seed=n + m + k)
 
 
-@pytest.mark.parametrize("n,m,k", [(1, 7168, 8192), (4, 130, 20000), (40, 300, 1680), (300, 513, 1040)])
+@pytest.mark.parametrize("n,m,k", [(1, 7168, 8192), (4, 130, 20000), (40, 300, 1680), (300, 513, 1040),
+                                   (1100, 2049, 528)])
 def test_product_of_small_integers_is_exact(n, m, k):
     """Codes of integers in [-2, 2] and power-of-two scales: every partial sum is exact."""
     g = gen(n + k)
@@ -164,7 +167,7 @@ def test_product_of_small_integers_is_exact(n, m, k):
     assert torch.equal(y.double(), X @ W.T)
 
 
-@pytest.mark.parametrize("n,m,k", [(8, 2304, 7168), (100, 1000, 3000 // 16 * 16), (260, 390, 2064)])
+@pytest.mark.parametrize("n,m,k", [(8, 2304, 7168), (100, 1000, 2992), (260, 390, 2064), (1500, 2300, 528)])
 def test_product_repeats_bit_for_bit_and_leaves_its_workspace_ready(n, m, k):
     x, xs, w, wsc = product_case(n, m, k, 3)
     ws = sga.alloc_gemm_fp8_workspace()
