@@ -148,12 +148,21 @@ struct StreamParams {
   bool w_static;
 };
 
-__device__ __forceinline__ void store_y(const StreamParams& p, int row, int token, float v) {
-  const size_t i = static_cast<size_t>(token) * p.m + row;
+// y[token0 + i * stride][row] = value(i) for i < count (at most kMost, unrolled).
+template <int kMost, class Value>
+__device__ __forceinline__ void store_y(const StreamParams& p, int row, int token0, int stride, int count,
+                                        Value value) {
+  const size_t at = static_cast<size_t>(token0) * p.m + row, step = static_cast<size_t>(stride) * p.m;
   if (p.out_bf16) {
-    p.out_bf16[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    uint16_t* o = p.out_bf16 + at;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i, o += step)
+      if (i < count) *o = __bfloat16_as_ushort(__float2bfloat16_rn(value(i)));
   } else {
-    p.out_f32[i] = v;
+    float* o = p.out_f32 + at;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i, o += step)
+      if (i < count) *o = value(i);
   }
 }
 
@@ -436,11 +445,8 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
         if (slot == 0) sph ^= 1u;
       }
       const int row = t / p.n_blocks * kTileM + mrow, token0 = t % p.n_blocks * NP + col0;
-      if (ok && p.splits == 1 && row < p.m) {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (token0 + i < p.n) store_y(p, row, token0 + i, acc[i]);
-      }
+      if (ok && p.splits == 1 && row < p.m)
+        store_y<kCols>(p, row, token0, 1, p.n - token0, [&](int i) { return acc[i]; });
     }
     if (!ok && lane == 0) {
       record_status(p.status, kStatusTimeout);
@@ -466,12 +472,17 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
       const int row = first / p.n_blocks * kTileM + mrow, token0 = first % p.n_blocks * NP;
       const float* part = reinterpret_cast<const float*>(smem) + mrow;
       if (ok && row < p.m) {
+        // this warp's half of the tokens, eight at a time: their partial sums loaded together
         const int last = min(c1, p.n - token0);
-#pragma unroll 4
-        for (int i = c0 + (warp - 4) / 4; i < last; i += Cfg::kGroups) {
-          float sum = 0.f;
-          for (int r = 0; r < S; ++r) sum += part[(r * width + i - c0) * kTileM];
-          store_y(p, row, token0 + i, sum);
+        for (int i0 = c0 + (warp - 4) / 4; i0 < last; i0 += 8 * Cfg::kGroups) {
+          float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          for (int r = 0; r < S; ++r) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)  // past the last token: any of the buffer's values
+              sum[q] += part[(r * width + min(i0 + q * Cfg::kGroups, last - 1) - c0) * kTileM];
+          }
+          store_y<8>(p, row, token0 + i0, Cfg::kGroups, (last - i0 + Cfg::kGroups - 1) / Cfg::kGroups,
+                     [&](int q) { return sum[q]; });
         }
       }
     }
