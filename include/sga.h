@@ -284,12 +284,6 @@ SGA_API sga_status_t sga_quantize_fp8(int32_t rows, int32_t cols, const sga_bf16
 
 typedef enum { SGA_OUT_FP32 = 0, SGA_OUT_BF16 = 1 } sga_out_type_t;
 
-/* Bytes of workspace sga_gemm_fp8 needs, whatever the sizes: a status word,
- * counters and the fp32 partial sums of output tiles that several thread blocks
- * share.  Zero-filled before the first call; every call leaves the counters
- * zeroed for the next one (after a device error, zero it again). */
-#define SGA_GEMM_FP8_WORKSPACE_BYTES (24 * 1024 * 1024)
-
 /* The block-scaled product y = x w^T of n tokens and m output channels:
  *   y[t][i] = sum_j x_scale[t][j] w_scale[i / 128][j]
  *             sum_{c in block j of 128} x[t][c] w[i][c]
@@ -300,7 +294,7 @@ typedef enum { SGA_OUT_FP32 = 0, SGA_OUT_BF16 = 1 } sga_out_type_t;
  * the tensor core, the scaled blocks in fp32 in a fixed order (results do not
  * depend on the schedule); a bf16 y is rounded once.  k is a multiple of 16; x
  * and w 16-byte aligned, y aligned to its elements.  The last blocks may be
- * partial. */
+ * partial.  Workspace: the status word only, 256 bytes. */
 SGA_API sga_status_t sga_gemm_fp8(int32_t n, int32_t m, int32_t k, const sga_fp8_e4m3_t* x, const float* x_scale,
                                   const sga_fp8_e4m3_t* w, const float* w_scale, void* y, sga_out_type_t out_type,
                                   void* ws, size_t ws_bytes, sga_stream_t stream);

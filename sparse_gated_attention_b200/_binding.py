@@ -47,7 +47,6 @@ EXPORTED = ["sga_abi_version", "sga_status_string", "sga_workspace_size", "sga_i
 NOALLOC_SCRATCH_BYTES = 256 + 4 * 1024 * 1024
 KV4_ROW_BYTES = 416  # one row of the 4-bit latent cache (see sga_kv4_append)
 FP8_BLOCK = 128  # channels (and weight rows) that share a scale
-GEMM_FP8_WORKSPACE_BYTES = 24 * 1024 * 1024
 STATUS_BYTES = 256  # the workspace of a call that keeps only its status word there
 _OUT_TYPES = {torch.float32: 0, torch.bfloat16: 1}  # sga_out_type_t
 
@@ -516,11 +515,6 @@ def _gemm_fp8_shapes(x_shape, w_shape):
     return n, (*lead, kb), (-(-M // FP8_BLOCK), kb), (*lead, M)
 
 
-def alloc_gemm_fp8_workspace(device=None) -> torch.Tensor:
-    """A zero-filled workspace for gemm_fp8, of any sizes."""
-    return torch.zeros(GEMM_FP8_WORKSPACE_BYTES, dtype=torch.uint8, device=device or "cuda")
-
-
 def gemm_fp8(x, x_scale, w, w_scale, out_dtype=torch.float32, out=None, ws=None, stream=None):
     """The product x w^T of E4M3 activations x [..., K] and weights w [M, K] with the scales x_scale
     [..., ceil(K / 128)] and w_scale [ceil(M / 128), ceil(K / 128)] fp32 (sga_gemm_fp8) -> [..., M], fp32 or bf16."""
@@ -541,7 +535,7 @@ def gemm_fp8(x, x_scale, w, w_scale, out_dtype=torch.float32, out=None, ws=None,
     else:
         _need(out, "out", out_dtype, y_shape)
     if ws is None:
-        ws = alloc_gemm_fp8_workspace(x.device)
+        ws = _status_ws(x.device)
     _one_device(x, x_scale, w, w_scale, out, ws)
     st = (_lib or load_library()).sga_gemm_fp8(
         n, M, K, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), kind,

@@ -9,15 +9,18 @@
 // added to fp32 accumulators in registers with its scale, while the tensor core
 // works on the next block.
 //
-// gemm_fp8_stream_kernel: the weights are the M = 128 operand, so that one
-// weight scale belongs to the whole tile and block, and a tile of output
-// channels is consecutive over the lanes when it is written; the tokens are N
-// (16 to 128 at a time).  For few tokens the weights are the whole cost: the
-// work (tiles x pairs of K blocks) is cut into one equal range for each SM
-// whatever the tile count, so every SM streams the same number of weight bytes.
-// A tile that several ranges share is summed by whichever of them arrives last,
-// over the partial sums in the workspace in range order: the result does not
-// depend on the schedule, and no second launch is needed.
+// gemm_fp8_stream_kernel, few tokens or few tiles: the weights are the M = 128 operand, so that one weight scale belongs
+// to the whole tile and block, and a thread's outputs are consecutive over the lanes; the tokens are N (16 to 128 at a
+// time).  Bound by the weights' bytes, or where those are few by the latency of the chain (load, MMA, TMEM read, output).
+// Where the tiles do not fill the SMs, K is split over a cluster whose thread blocks add up each other's partial sums
+// through distributed shared memory, in a fixed order: the result does not depend on the schedule, and no second launch is
+// needed.  (Sums in global memory by whichever block arrived last cost 4 to 6 us more.)  4 x 2304 x 7168 (n x m x k)
+// 7.0 us, 2.4 TB/s; 32 x 20544 x 1536 8.8 us, 3.8 TB/s; 256 x 2304 x 7168 16.0 us.
+//
+// gemm_fp8_tile_kernel, many tokens: pairs of CTAs, 256 tokens x 256 channels a tile, the tokens as M.  Bound by the
+// hand-over between the MMA (512 cycles a K block) and the scaled sums in registers (450 cycles) over two accumulators of
+// 256 columns, and by power at large sizes: 4096 x 7168 x 8192 253 us on zeros, 291 on data, 1.65 PFLOP/s (the MMAs alone
+// 147).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -285,10 +288,11 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
       if (!ok) {
         record_status(p.status, kStatusTimeout);
         *abort_flag = 1;
-        volatile int never = 0;
-        for (long long i = (issued > Cfg::kStages ? issued - Cfg::kStages : 0); i < issued; ++i)
-          mbar_wait(full(static_cast<int>(i % Cfg::kStages)), static_cast<uint32_t>((i / Cfg::kStages) & 1), &never);
       }
+      // The copies in flight land before the ring is reused and the thread block exits, also when the MMA warp gave up.
+      volatile int never = 0;
+      for (long long i = (issued > Cfg::kStages ? issued - Cfg::kStages : 0); i < issued; ++i)
+        mbar_wait(full(static_cast<int>(i % Cfg::kStages)), static_cast<uint32_t>((i / Cfg::kStages) & 1), &never);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -504,22 +508,24 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
 constexpr int kClusters[kMaxSplits] = {148, 74, 45, 33, 26, 22, 15, 15};
 
 // What the kernel takes for `tiles` tiles of NP tokens, in microseconds, and the split of K it takes it with.  Fitted to
-// runs of 1 to 8 splits at 300 x 4096, 300 x 512, 2304 x 1536 and 1111 x 1552 weights with 8, 32, 64 and 96 tokens: a
-// unit 0.6 (16 tokens) to 0.9 us (128 tokens); a split's barriers 1 us and its exchange and sum 2.5 to 5 us shared out over
-// its thread blocks (two units in one thread block 3.5 us, in two 5.1; sixteen in one 12.0, in eight 4.7).  Only splits
-// whose clusters all run at once are considered.
+// runs of 1 to 8 splits at 300 x 2048, 300 x 8192 and 1900 x 4096 weights with 8, 32, 64 and 96 tokens: a unit 0.43 (16
+// tokens) to 0.85 us (128 tokens), an exchange 1 to 3 us and 0.3 us for each thread block that joins it, another
+// tile's output 2 us.  300 x 2048, 8
+// tokens: 5.6 us unsplit, 4.4 in four, 4.4 in eight; 300 x 8192: 15.8, 6.9, 5.5.  Only splits whose clusters all run at
+// once are considered.
 struct StreamPlan {
   int splits;
   float us;
 };
 StreamPlan stream_plan(int np, long long tiles, int units) {
-  const float unit = 0.57f + 0.0026f * np;
-  const float base = 1.7f + 0.035f * np;
-  StreamPlan best = {1, base + unit * static_cast<float>(units) * static_cast<float>((tiles + 147) / 148)};
+  const float unit = 0.42f + 0.000026f * np * np;
+  const float base = 2.3f + 0.004f * np;
+  const float waves = static_cast<float>((tiles + 147) / 148);
+  StreamPlan best = {1, base + unit * static_cast<float>(units) * waves + 2.f * (waves - 1.f)};
   for (int splits = 2; splits <= kMaxSplits && splits <= units; ++splits) {
     if (tiles > kClusters[splits - 1]) break;
-    const float us = base + unit * static_cast<float>((units + splits - 1) / splits) + 1.f +
-                     (2.2f + 0.022f * np) / static_cast<float>(splits);
+    const float us = base + unit * static_cast<float>((units + splits - 1) / splits) + 0.1f + 0.0185f * np +
+                     0.3f * static_cast<float>(splits);
     if (us < best.us) best = {splits, us};
   }
   return best;
@@ -705,11 +711,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!ok) {
           record_status(p.status, kStatusTimeout);
           *abort_flag = 1;
-          volatile int never = 0;
-          if (rank == 0)  // the peer waits for the leader at the cluster barrier below
-            for (long long i = (issued > kTStages ? issued - kTStages : 0); i < issued; ++i)
-              mbar_wait_idle(full(static_cast<int>(i % kTStages)), static_cast<uint32_t>((i / kTStages) & 1), &never);
         }
+        // The copies in flight land before the pair exits, also when an MMA warp gave up (the peer waits for the leader
+        // at the cluster barrier below).
+        volatile int never = 0;
+        if (rank == 0)
+          for (long long i = (issued > kTStages ? issued - kTStages : 0); i < issued; ++i)
+            mbar_wait_idle(full(static_cast<int>(i % kTStages)), static_cast<uint32_t>((i / kTStages) & 1), &never);
       }
     } else if (warp < 3) {
       // ---------------------------------------------------------- MMA issuers (of the leader, for both CTAs)
@@ -957,13 +965,14 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   if (a.n <= 16) return launch_stream<16>(a, num_sms, s);
   if (a.n <= 32) return launch_stream<32>(a, num_sms, s);
   if (a.n <= 64) return launch_stream<64>(a, num_sms, s);
-  // More tokens: blocks of 128 through the streaming kernel, whose split K shortens a product of few tiles, or tiles of
-  // 256 x 256, each over the whole of K (0.5 us a K block), which read the operands less often.  256 tokens, m x k of
-  // 2304 x 7168: 19.6 us against 34.8; 400 tokens, 7168 x 8192: 64.2 against 40.3.
+  // More tokens: blocks of 128 through the streaming kernel, whose split K or smaller tiles fill the SMs where there are
+  // few, or tiles of 256 x 256, which read the operands less often (a K block 0.47 us, another tile's output 5 us).
+  // n x m x k, streaming against tiles: 256 x 2304 x 7168 16.0 us against 34.6, 512 x 4096 x 4096 17.7 against 23.4;
+  // 700 x 4096 x 4096 31.9 against 24.1, 400 x 7168 x 8192 58.6 against 39.9.
   const long long k_blocks = (a.k + kBlock - 1) / kBlock;
   const long long m128 = (a.m + kTileM - 1) / kTileM, n128 = (a.n + 127) / 128;
   const long long waves = (((a.m + kTN - 1) / kTN) * static_cast<long long>((a.n + 2 * kTM - 1) / (2 * kTM)) + 73) / 74;
-  const float tile_us = 6.f + 0.5f * static_cast<float>(k_blocks * waves);
+  const float tile_us = 7.f + 0.47f * static_cast<float>(k_blocks * waves) + 5.f * static_cast<float>(waves - 1);
   if (stream_plan(128, m128 * n128, static_cast<int>((k_blocks + kUnit - 1) / kUnit)).us < tile_us)
     return launch_stream<128>(a, num_sms, s);
   return launch_tile(a, num_sms, s);
@@ -995,13 +1004,13 @@ sga_status_t sga_gemm_fp8(int32_t n, int32_t m, int32_t k, const sga_fp8_e4m3_t*
   if (!aligned(x, 16) || !aligned(x_scale, 4) || !aligned(w, 16) || !aligned(w_scale, 4) ||
       !aligned(y, out_type == SGA_OUT_FP32 ? 4 : 2))
     return SGA_ERR_INVALID_ARG;
-  if (!aligned(ws, sga::host::kWsAlign) || ws_bytes < SGA_GEMM_FP8_WORKSPACE_BYTES) return SGA_ERR_WORKSPACE;
+  if (!aligned(ws, sga::host::kWsAlign) || ws_bytes < sga::host::kStatusBytes) return SGA_ERR_WORKSPACE;
   int sms = 0;
   const sga_status_t st = sga::host::device_info(&sms);
   if (st != SGA_OK) return st;
   sga::host::NvtxRange range("sga.gemm_fp8");
   sga::GemmFp8Args a{n, m, k, x, x_scale, w, w_scale, out_type == SGA_OUT_FP32 ? static_cast<float*>(y) : nullptr,
-                     out_type == SGA_OUT_BF16 ? static_cast<uint16_t*>(y) : nullptr, ws, static_cast<int*>(ws)};
+                     out_type == SGA_OUT_BF16 ? static_cast<uint16_t*>(y) : nullptr, static_cast<int*>(ws)};
   return sga::host::from_cuda(sga::launch_gemm_fp8(a, sms, static_cast<cudaStream_t>(stream)));
 }
 

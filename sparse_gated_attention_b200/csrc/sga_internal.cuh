@@ -116,7 +116,6 @@ struct GemmFp8Args {
   const float* w_scale;  // [ceil(m / 128)][ceil(k / 128)]
   float* out_f32;        // [n][m], or null
   uint16_t* out_bf16;    // [n][m], or null
-  void* ws;              // SGA_GEMM_FP8_WORKSPACE_BYTES, counters zero
   int* status;
   bool w_static = false;  // no earlier kernel of the stream writes w: it may be read before they finish
 };

@@ -477,7 +477,7 @@ constexpr int kCqRows8 = kQIdxOff8 + kIdxHeads * kIdxDim;       // 20,608
 
 struct LayerLayout8 {
   size_t path_bytes = 0;  // sga_forward_kv4's workspace, at the start (its status word is the layer's)
-  size_t gemm = 0, codes = 0, scale = 0, g1 = 0, c_q = 0, g2 = 0, q_nope = 0, q = 0, gate = 0, q_idx = 0, w = 0;
+  size_t codes = 0, scale = 0, g1 = 0, c_q = 0, g2 = 0, q_nope = 0, q = 0, gate = 0, q_idx = 0, w = 0;
   size_t kv_rows = 0, out_b = 0, o_b = 0, total = 0;
 };
 
@@ -502,7 +502,6 @@ sga_status_t layer_layout8(const sga_dims_t& d, int d_model, int q_rank, LayerLa
     return at_off;
   };
   const size_t widest = std::max<size_t>(std::max(d_model, q_rank), kOWidth);
-  l->gemm = take(SGA_GEMM_FP8_WORKSPACE_BYTES);
   l->codes = take(rows * widest);
   l->scale = take(rows * ((widest + kBlock8 - 1) / kBlock8) * 4);
   l->g1 = take(rows * (ceil_block8(q_rank) + kHqExtra8) * 4);
@@ -527,7 +526,7 @@ cudaError_t quantized_product(const uint16_t* x, int rows, int k, const sga_fp8_
   float* scale = at<float>(ws, l.scale);
   const cudaError_t e = sga::launch_quantize_fp8(rows, k, x, codes, scale, s);
   if (e != cudaSuccess) return e;
-  sga::GemmFp8Args a{rows, m, k, codes, scale, w, w_scale, y, nullptr, at<void>(ws, l.gemm), at<int>(ws, 0)};
+  sga::GemmFp8Args a{rows, m, k, codes, scale, w, w_scale, y, nullptr, at<int>(ws, 0)};
   a.w_static = true;
   return sga::launch_gemm_fp8(a, sms, s);
 }

@@ -124,7 +124,7 @@ def product_case(n, m, k, seed):
 
 def check_product(n, m, k, out_dtype, seed=0, ws=None):
     x, xs, w, wsc = product_case(n, m, k, seed)
-    ws = sga.alloc_gemm_fp8_workspace() if ws is None else ws
+    ws = status_ws() if ws is None else ws
     y = sga.gemm_fp8(x, xs, w, wsc, out_dtype=out_dtype, ws=ws)
     assert y.dtype == out_dtype and tuple(y.shape) == (n, m)
     assert sga.device_status(ws) == 0
@@ -170,11 +170,11 @@ def test_product_of_small_integers_is_exact(n, m, k):
 @pytest.mark.parametrize("n,m,k", [(8, 2304, 7168), (100, 1000, 2992), (260, 390, 2064), (1500, 2300, 528)])
 def test_product_repeats_bit_for_bit_and_leaves_its_workspace_ready(n, m, k):
     x, xs, w, wsc = product_case(n, m, k, 3)
-    ws = sga.alloc_gemm_fp8_workspace()
+    ws = status_ws()
     first = sga.gemm_fp8(x, xs, w, wsc, ws=ws)
     for _ in range(5):
         assert torch.equal(sga.gemm_fp8(x, xs, w, wsc, ws=ws), first)
-    assert int(ws[:1280].to(torch.int64).sum()) == 0  # status and counters
+    assert int(ws.to(torch.int64).sum()) == 0
     check_product(n + 1, m, k, torch.bfloat16, seed=9, ws=ws)  # other sizes, same workspace
 
 
@@ -454,7 +454,7 @@ def test_calls_on_another_stream_and_in_a_graph():
     g = gen(15)
     x = randn(g, 5, 512).to(torch.bfloat16)
     w, wsc = rand_codes(g, 300, 512), torch.rand((3, 4), generator=g, device=DEV) + 0.5
-    ws = sga.alloc_gemm_fp8_workspace()
+    ws = status_ws()
     rows = randn(g, 2, 1, 576).to(torch.bfloat16)
     cache = fill_cache(g, 2, 200)
     pos = torch.tensor([[3], [199]], dtype=torch.int32, device=DEV)
@@ -489,12 +489,12 @@ def test_calls_on_another_stream_and_in_a_graph():
     assert sga.device_status(ws) == 0 and sga.device_status(ws2) == 0
 
 
-def test_two_streams_at_once_with_their_own_workspaces():
+def test_two_streams_at_once():
     cases = [product_case(40, 2304, 1536, 21), product_case(200, 1000, 2048, 22)]
     want = [sga.gemm_fp8(*c) for c in cases]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in cases]
-    spaces = [sga.alloc_gemm_fp8_workspace() for _ in cases]
+    spaces = [status_ws() for _ in cases]
     torch.cuda.synchronize()
     outs = [[], []]
     for _ in range(10):
@@ -604,7 +604,7 @@ def test_python_refusals():
     with pytest.raises(sga.SGAError):  # k not a multiple of 16
         sga.gemm_fp8(x[:, :24].contiguous(), xs[:, :1].contiguous(), w[:, :24].contiguous(), wsc[:, :1].contiguous())
     with pytest.raises(sga.SGAError):  # workspace too small
-        sga.gemm_fp8(x, xs, w, wsc, ws=status_ws())
+        sga.gemm_fp8(x, xs, w, wsc, ws=status_ws()[:128])
     with pytest.raises(TypeError):
         sga.quantize_fp8(torch.zeros((2, 32), device=DEV))
     with pytest.raises(sga.SGAError):

@@ -126,15 +126,13 @@ def test_quantize_refuses_bad_arguments(lib):
 
 
 def test_product_refuses_bad_arguments(lib):
-    big = sga.GEMM_FP8_WORKSPACE_BYTES
-
-    def call(n=4, m=5, k=32, x=GOOD, xs=GOOD, w=GOOD, wsc=GOOD, y=GOOD, t=0, ws=WS, nbytes=big):
+    def call(n=4, m=5, k=32, x=GOOD, xs=GOOD, w=GOOD, wsc=GOOD, y=GOOD, t=0, ws=WS, nbytes=256):
         return lib.sga_gemm_fp8(n, m, k, x, xs, w, wsc, y, t, ws, nbytes, None)
 
     for bad in [dict(n=0), dict(m=0), dict(k=0), dict(k=24), dict(n=-3), dict(t=2), dict(x=None), dict(x=ODD),
                 dict(w=ODD), dict(xs=ODD), dict(wsc=None), dict(y=None), dict(y=ODD), dict(y=P(0x100001), t=1)]:
         assert call(**bad) == 1, bad
-    for bad in [dict(ws=None), dict(ws=P(0x20000010)), dict(nbytes=big - 1)]:
+    for bad in [dict(ws=None), dict(ws=P(0x20000010)), dict(nbytes=255)]:
         assert call(**bad) == 3, bad
 
 
@@ -165,10 +163,10 @@ def _fp8_weights(d_model=7168, q_rank=1536, **bad):
 def test_layer_fp8kv4_workspace_and_refusals(lib):
     d = sga.make_dims(32, 1, 131072)
     size = sga.layer_fp8kv4_workspace_size(d, _fp8_weights())
-    assert size >= sga.workspace_size(d) + sga.GEMM_FP8_WORKSPACE_BYTES + 32 * 4 * (20608 + 1536 + 832)
+    assert size >= sga.workspace_size(d) + 32 * 4 * (20608 + 1536 + 832)
     r, big = ctypes.byref(d), 1 << 40
 
-    def call(W=_fp8_weights(), dims=r, h=GOOD, pos=GOOD, kv4=GOOD, k=GOOD, idx=None, y=GOOD, ws=WS, nbytes=big):
+    def call(W=_fp8_weights(), dims=r, h=GOOD, pos=GOOD, kv4=GOOD, k=GOOD, idx=None, y=GOOD, ws=WS, nbytes=256):
         return lib.sga_layer_forward_fp8kv4(dims, ctypes.byref(W), h, pos, kv4, k, idx, y, ws, nbytes, None)
 
     for W in (_fp8_weights(d_model=7160), _fp8_weights(q_rank=1528), _fp8_weights(d_model=0), _fp8_weights(w_hq=0),
