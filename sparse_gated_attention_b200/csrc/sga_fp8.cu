@@ -504,9 +504,6 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
   }
 }
 
-// Clusters of 1 .. 8 thread blocks (one per SM) that a B200 holds at a time.
-constexpr int kClusters[kMaxSplits] = {148, 74, 45, 33, 26, 22, 15, 15};
-
 // What the kernel takes for `tiles` tiles of NP tokens, in microseconds, and the split of K it takes it with.  Fitted to
 // runs of 1 to 8 splits at 300 x 2048, 300 x 8192 and 1900 x 4096 weights with 8, 32, 64 and 96 tokens: a unit 0.43 (16
 // tokens) to 0.85 us (128 tokens), an exchange 1 to 3 us and 0.3 us for each thread block that joins it, another
@@ -523,7 +520,7 @@ StreamPlan stream_plan(int np, long long tiles, int units) {
   const float waves = static_cast<float>((tiles + 147) / 148);
   StreamPlan best = {1, base + unit * static_cast<float>(units) * waves + 2.f * (waves - 1.f)};
   for (int splits = 2; splits <= kMaxSplits && splits <= units; ++splits) {
-    if (tiles > kClusters[splits - 1]) break;
+    if (tiles > host::kClusters[splits - 1]) break;
     const float us = base + unit * static_cast<float>((units + splits - 1) / splits) + 0.1f + 0.0185f * np +
                      0.3f * static_cast<float>(splits);
     if (us < best.us) best = {splits, us};

@@ -13,6 +13,9 @@ namespace sga {
 namespace host {
 
 constexpr size_t kWsAlign = 256;      // every workspace region starts on this boundary
+// Clusters of 1 .. 8 thread blocks (one per SM) that a B200 holds at a time: its SMs are in groups of unequal size, which
+// clusters do not cross.
+constexpr int kClusters[8] = {148, 74, 45, 33, 26, 22, 15, 15};
 constexpr size_t kStatusBytes = 256;  // the status block at the start of a workspace
 
 inline size_t align_up(size_t x) { return (x + kWsAlign - 1) / kWsAlign * kWsAlign; }

@@ -311,7 +311,7 @@ def pick(g, B, T, L, K, fill=1.0):
 
 ATTEND_CASES = [(1, 1, 64, 64, 1.0), (1, 1, 1, 64, 1.0), (2, 1, 3000, 2048, 1.0), (1, 3, 700, 128, 0.5),
                 (3, 2, 300, 192, 1.0), (20, 1, 500, 320, 0.7), (2, 5, 1001, 1088, 0.9), (40, 4, 200, 256, 0.8),
-                (1, 150, 400, 128, 1.0)]
+                (1, 150, 400, 128, 1.0), (18, 1, 1200, 1024, 1.0), (31, 5, 90, 192, 0.9)]
 
 
 @pytest.mark.parametrize("gated", [True, False])
@@ -322,6 +322,25 @@ def test_attend_kv4_matches_definition(B, T, L, K, fill, gated):
     q = randn(g, B, T, 64, 576).to(torch.bfloat16)
     gate = randn(g, B, T, 64).to(torch.bfloat16) if gated else None
     check_attend(q, cache, pick(g, B, T, L, K, fill), gate)
+
+
+def test_attend_kv4_next_call_reads_every_row():
+    """The quantiser, launched right behind, sees the output of all 301 queries (two full waves and five split ones)."""
+    g = gen(18)
+    cache = fill_cache(g, 1, 600)
+    q = randn(g, 1, 301, 64, 576).to(torch.bfloat16)
+    idx = pick(g, 1, 301, 600, 512)
+    out = torch.empty((1, 301, 64, 512), dtype=torch.bfloat16, device=DEV)
+    codes = torch.empty((301, 64 * 512), dtype=torch.float8_e4m3fn, device=DEV)
+    want = sga.sparse_mla_attend_kv4(q, cache, idx)
+    want_codes, want_scale = sga.quantize_fp8(want.view(301, -1))
+    for _ in range(5):
+        out.zero_()
+        codes.view(torch.uint8).zero_()
+        sga.sparse_mla_attend_kv4(q, cache, idx, out=out)
+        scale = sga.quantize_fp8(out.view(301, -1), codes=codes)[1]
+        assert torch.equal(codes.view(torch.uint8), want_codes.view(torch.uint8)) and torch.equal(scale, want_scale)
+        assert torch.equal(out, want)
 
 
 def test_attend_kv4_empty_and_sparse_rows():
