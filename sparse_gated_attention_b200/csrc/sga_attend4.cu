@@ -99,6 +99,27 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// (a, b) = (a, b) * s + c, and (a, b) += (x, y): two lanes an instruction.
+__device__ __forceinline__ void fma2(float& a, float& b, float s, float c) {
+  asm("{\n\t.reg .b64 v, t, u;\n\t"
+      "mov.b64 v, {%0, %1};\n\t"
+      "mov.b64 t, {%2, %2};\n\t"
+      "mov.b64 u, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, v, t, u;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 v, t;\n\t"
+      "mov.b64 v, {%0, %1};\n\t"
+      "mov.b64 t, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, t;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -516,68 +537,90 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
           }
         }
       }
-      float alpha[2];
-      bool resc = false;
+      // The weights are computed with the running maximum so far, and again if this chunk passes it by more than the
+      // threshold (or is the first).
+      float mt[2], ps[2];
+      uint32_t x[16];  // x[2k + i]: the weights of head i at columns 8k + 2 m4 and 8k + 2 m4 + 1
+      bool need = false;
+      const auto weights = [&] {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // every slot so far empty: -inf - 0, all weights zero
+          const float m_p = m_ref[i] == -INFINITY ? 0.f : m_ref[i] - kPShift;
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+          const bool exact = fabsf(m_p) < 0x1p20f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float v0 = r[4 * k + 2 * i], v1 = r[4 * k + 2 * i + 1];
+            if (exact) {
+              fma2(v0, v1, sc[i], -m_p);
+            } else {  // scaled first and rounded, so that the maximum's difference is exact however large the scores are
+              v0 = __fsub_rn(__fmul_rn(v0, sc[i]), m_p);
+              v1 = __fsub_rn(__fmul_rn(v1, sc[i]), m_p);
+            }
+            v0 = fast_exp2(v0);
+            v1 = fast_exp2(v1);
+            x[2 * k + i] = pack_f16(v0, v1);
+            add2(s[2 * (k & 1)], s[2 * (k & 1) + 1], v0, v1);
+          }
+          ps[i] = (s[0] + s[1]) + (s[2] + s[3]);
+        }
+      };
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float mp[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           mp[c] = fmaxf(fmaxf(r[8 * c + 2 * i], r[8 * c + 2 * i + 1]), fmaxf(r[8 * c + 4 + 2 * i], r[8 * c + 5 + 2 * i]));
-        float mt = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
-        mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 1));
-        mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 2)) * sc[i];  // the scale is positive
-        alpha[i] = 1.f;
-        if (m_ref[i] == -INFINITY) {
-          m_ref[i] = mt;  // nothing accumulated yet (all earlier weights were zero)
-        } else if (mt > m_ref[i] + kRescaleThreshold) {
-          alpha[i] = exp2f(m_ref[i] - mt);
-          m_ref[i] = mt;
-          resc = true;
-        }
-        // weights of the row, in place of its scores; every slot so far empty: -inf - 0, all weights zero
-        const float m_p = m_ref[i] == -INFINITY ? 0.f : m_ref[i] - kPShift;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        mt[i] = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+      }
+      weights();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // scaled first and rounded, so that the maximum's difference is exact however large the scores are
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = fast_exp2(__fsub_rn(__fmul_rn(r[4 * k + 2 * i + e], sc[i]), m_p));
-            r[4 * k + 2 * i + e] = x;
-            ps[2 * (k & 1) + e] += x;
-          }
-        }
-        l_run[i] = l_run[i] * alpha[i] + ((ps[0] + ps[1]) + (ps[2] + ps[3]));  // this thread's columns
+      for (int i = 0; i < 2; ++i) {
+        mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xFFFFFFFFu, mt[i], 1));
+        mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xFFFFFFFFu, mt[i], 2)) * sc[i];  // the scale is positive
+        need |= !(mt[i] <= m_ref[i] + kRescaleThreshold);                       // also for a NaN
       }
       // PV_{j-1} must be done before P and O are touched.
       ok = ok && mbar_wait(p_free, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag);
       tc_fence_after();
-      if (m4 == 0) {
-        head_f[hrow[0]] = alpha[0];
-        head_f[hrow[1]] = alpha[1];
-      }
-      if (named_barrier_or(1, kSoftmaxThreads, resc)) {
-        // O^T[dim][head] *= alpha[head]: every lane holds one dim of each block
-        for (int blk = 0; blk < 4; ++blk) {
-          for (int c = 0; c < 2; ++c) {
-            float o[32];
-            tmem_ld32(tmem + lane_addr + blk * kHeads + c * 32, o);
+      if (named_barrier_or(1, kSoftmaxThreads, need)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= head_f[c * 32 + i];
-            tmem_st32(tmem + lane_addr + blk * kHeads + c * 32, o);
+        for (int i = 0; i < 2; ++i) {
+          float alpha = 1.f;
+          if (m_ref[i] == -INFINITY) {
+            m_ref[i] = mt[i];  // nothing accumulated yet (all earlier weights were zero)
+          } else if (mt[i] > m_ref[i] + kRescaleThreshold) {
+            alpha = exp2f(m_ref[i] - mt[i]);
+            m_ref[i] = mt[i];
           }
+          l_run[i] *= alpha;
+          if (m4 == 0) head_f[hrow[i]] = alpha;
         }
-        named_barrier(1, kSoftmaxThreads);
+        weights();
+        if (j > 0) {
+          named_barrier(1, kSoftmaxThreads);
+          // O^T[dim][head] *= alpha[head]: every lane holds one dim of each block
+          for (int blk = 0; blk < 4; ++blk) {
+            for (int c = 0; c < 2; ++c) {
+              float o[32];
+              tmem_ld32(tmem + lane_addr + blk * kHeads + c * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= head_f[c * 32 + i];
+              tmem_st32(tmem + lane_addr + blk * kHeads + c * 32, o);
+            }
+          }
+          named_barrier(1, kSoftmaxThreads);
+        }
       }
+      l_run[0] += ps[0];  // this thread's columns
+      l_run[1] += ps[1];
       // P[head][row] in the 128-byte-swizzled K-major layout (8 heads per 1 KB atom).  A thread's values are two
       // columns of row t/4 of 8 x 8 blocks, the layout stmatrix takes: four blocks (two of heads, two of columns)
       // at a time, the row addresses from lanes 8 b .. 8 b + 7 for block b.
 #pragma unroll
       for (int k = 0; k < 8; k += 2)
-        stmatrix_x4(p_row + (((k + (lane >> 4)) ^ (lane & 7)) << 4), pack_f16(r[4 * k], r[4 * k + 1]),
-                    pack_f16(r[4 * k + 2], r[4 * k + 3]), pack_f16(r[4 * k + 4], r[4 * k + 5]),
-                    pack_f16(r[4 * k + 6], r[4 * k + 7]));
+        stmatrix_x4(p_row + (((k + (lane >> 4)) ^ (lane & 7)) << 4), x[2 * k], x[2 * k + 1], x[2 * k + 2], x[2 * k + 3]);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);  // P_j and any rescale of O
