@@ -208,7 +208,7 @@ SGA_API sga_status_t sga_forward_fused_fp8(const sga_dims_t* dims, const sga_fp8
  * The latent cache in 4 bits (arXiv abstract "A.X K2 Technical Report": the
  * model is served in NVFP4; archdb "A.X K2", KV fields: 512 latent + 64 rope
  * values per token).  A cache row is SGA_KV4_ROW_BYTES bytes, [B][L][416]
- * (16-byte aligned):
+ * (32-byte aligned):
  *   bytes   0..255  512 E2M1 codes (1 sign, 2 exponent, 1 mantissa bit:
  *                   +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}); byte j holds latent dim 2j
  *                   in its low half and dim 2j+1 in its high half

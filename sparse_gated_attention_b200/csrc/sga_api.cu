@@ -143,7 +143,7 @@ sga_status_t forward_impl(const sga_dims_t* dims, const void* q_idx, const sga_b
   if (!dims_ok(dims)) return SGA_ERR_INVALID_ARG;
   // with the 4-bit cache, kv4 and out_bf16 stand in the place of kv and out
   if (!aligned(q_idx, 16) || !aligned(w, 16) || !aligned(k_idx, 16) || !aligned(q, 16) ||
-      !aligned(kv4 ? static_cast<const void*>(kv4) : kv, 16) || !aligned(q_pos, 4) ||
+      !aligned(kv4 ? static_cast<const void*>(kv4) : kv, kv4 ? 32 : 16) || !aligned(q_pos, 4) ||
       !aligned(kv4 ? static_cast<void*>(out_bf16) : out, 16) || (gate && !aligned(gate, 2)) ||
       (idx_out && !aligned(idx_out, 16)) || (out_bf16 && !aligned(out_bf16, 8)))
     return SGA_ERR_INVALID_ARG;

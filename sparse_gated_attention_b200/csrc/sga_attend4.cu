@@ -42,9 +42,10 @@ constexpr int kDq = 576;
 constexpr int kDv = 512;
 constexpr int kChunk = 64;                   // selected rows per chunk
 constexpr int kBoxBytes = kChunk * 128;      // 64 rows x 64 dims of 16 bits
-constexpr int kPairBytes = 2 * kBoxBytes;    // 64 rows x 128 dims
-constexpr int kPairsPerChunk = 4;            // value dims 0..511
-constexpr int kPairRing = 8;                 // two chunks of value pairs
+constexpr int kPairBytes = 2 * kBoxBytes;    // 64 rows x 128 dims: A of one PV product
+constexpr int kHalfBytes = 2 * kPairBytes;   // 64 rows x 256 dims, filled and released together
+constexpr int kHalves = 2;                   // value dims 0..511
+constexpr int kRing = 2 * kHalves;           // two chunks of value tiles
 constexpr int kRopeRing = 2;
 constexpr int kQBox = kHeads * 128;          // 64 heads x 64 dims
 constexpr int kQBytes = 9 * kQBox;
@@ -58,11 +59,11 @@ constexpr int kSoftmaxThreads = 128;
 constexpr int kThreads = 32 * kSoftmaxWarp + kSoftmaxThreads;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;
-// barriers: pair_full[8] pair_empty[8] rope_full[2] rope_empty[2] q_full s_full[2] s_free[2]
+// barriers: full[4] empty[4] rope_full[2] rope_empty[2] q_full s_full[2] s_free[2]
 //           p_full p_free o_full qk_done
-constexpr int kNumBars = 2 * kPairRing + 2 * kRopeRing + 1 + 2 + 2 + 4;
+constexpr int kNumBars = 2 * kRing + 2 * kRopeRing + 1 + 2 + 2 + 4;
 constexpr int kMaxSplits = 8;                // splits of a query = CTAs of its cluster
-constexpr size_t kSmemBytes = 1024 + kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes + kPBytes +
+constexpr size_t kSmemBytes = 1024 + kRing * kHalfBytes + kRopeRing * kBoxBytes + kQBytes + kPBytes +
                               kNumBars * 8 + kMaskRing * 8 + 2 * kHeads * 4 + kHeads * 8 + 16;
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
 // P = 2^(x - max + 7): with a maximum that lags by at most 8 it stays within 2^15 and inside fp16, and fp16's
@@ -75,7 +76,7 @@ constexpr int kRopeOff = kScaleOff + kDv / 16;
 static_assert(kRowBytes == kRopeOff + 2 * (kDq - kDv), "cache row layout");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 // the split merge's receive buffer lies over the value ring, the rope slots and the Q buffer (see sga_attend.cu)
-static_assert(kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes >= 7 * kHeads * 76 * 4,
+static_assert(kRing * kHalfBytes + kRopeRing * kBoxBytes + kQBytes >= 7 * kHeads * 76 * 4,
               "split merge receive buffer");
 
 struct Attend4Params {
@@ -129,7 +130,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 16 bytes of the cache, read once per query: volatile keeps the load where it is issued, ahead of its use.
+// 32, 16 or 8 bytes, read once per query: volatile keeps the load where it is issued, ahead of its use.
+__device__ __forceinline__ void ld_row32(const uint8_t* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
 __device__ __forceinline__ uint4 ld_row16(const uint8_t* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -185,10 +191,10 @@ __device__ __forceinline__ uint4 expand_codes(uint32_t codes, uint32_t scale) {
   return v;
 }
 
-// The part of one cache row that one of its four producer threads (part = 0..3) expands: 32 codes of every
-// 128-dim pair, the scales of pair `part` (exchanged among the four threads) and 16 rope values.
+// The part of one cache row that one of its four producer threads (part = 0..3) expands: 64 codes of each half (the
+// half's box `part`), eight scales (exchanged among the four threads) and 16 rope values.
 struct RowPart {
-  uint4 codes[kPairsPerChunk];
+  uint4 codes[kHalves][2];
   uint2 scales;
   uint4 rope[2];
 };
@@ -196,13 +202,12 @@ struct RowPart {
 __device__ __forceinline__ void load_row(RowPart& d, const uint8_t* row, int part, bool valid) {
   if (valid) {
 #pragma unroll
-    for (int q = 0; q < kPairsPerChunk; ++q) d.codes[q] = ld_row16(row + 64 * q + 16 * part);
+    for (int h = 0; h < kHalves; ++h) ld_row32(row + 128 * h + 32 * part, d.codes[h][0], d.codes[h][1]);
     d.scales = ld_row8(row + kScaleOff + 8 * part);
-    d.rope[0] = ld_row16(row + kRopeOff + 32 * part);
-    d.rope[1] = ld_row16(row + kRopeOff + 32 * part + 16);
+    ld_row32(row + kRopeOff + 32 * part, d.rope[0], d.rope[1]);
   } else {  // an empty slot: zeros (masked out of the softmax)
 #pragma unroll
-    for (int q = 0; q < kPairsPerChunk; ++q) d.codes[q] = make_uint4(0, 0, 0, 0);
+    for (int h = 0; h < kHalves; ++h) d.codes[h][0] = d.codes[h][1] = make_uint4(0, 0, 0, 0);
     d.scales = make_uint2(0, 0);
     d.rope[0] = d.rope[1] = make_uint4(0, 0, 0, 0);
   }
@@ -212,17 +217,17 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t pairs = smem_u32(smem);
-  const uint32_t rope = pairs + kPairRing * kPairBytes;
+  const uint32_t rope = pairs + kRing * kHalfBytes;
   const uint32_t q_s = rope + kRopeRing * kBoxBytes;
   const uint32_t p_s = q_s + kQBytes;
-  uint8_t* p_ptr = smem + kPairRing * kPairBytes + kRopeRing * kBoxBytes + kQBytes;
+  uint8_t* p_ptr = smem + kRing * kHalfBytes + kRopeRing * kBoxBytes + kQBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(p_ptr + kPBytes);
   const uint32_t bar0 = smem_u32(bars);
-  auto pair_full = [&](int s) { return bar0 + 8u * s; };
-  auto pair_empty = [&](int s) { return bar0 + 8u * (kPairRing + s); };
-  auto rope_full = [&](int s) { return bar0 + 8u * (2 * kPairRing + s); };
-  auto rope_empty = [&](int s) { return bar0 + 8u * (2 * kPairRing + kRopeRing + s); };
-  const uint32_t q_full = bar0 + 8u * (2 * kPairRing + 2 * kRopeRing);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kRing + s); };
+  auto rope_full = [&](int s) { return bar0 + 8u * (2 * kRing + s); };
+  auto rope_empty = [&](int s) { return bar0 + 8u * (2 * kRing + kRopeRing + s); };
+  const uint32_t q_full = bar0 + 8u * (2 * kRing + 2 * kRopeRing);
   auto s_full = [&](int b) { return q_full + 8u * (1 + b); };
   auto s_free = [&](int b) { return q_full + 8u * (3 + b); };
   const uint32_t p_full = q_full + 8u * 5;
@@ -246,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
   const int slot_base = chunk0 * kChunk;                     // first selected slot of this split
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairRing; ++s) {
-      mbar_init(pair_full(s), kProducerWarps);
-      mbar_init(pair_empty(s), 1);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(full(s), kProducerWarps);
+      mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kRopeRing; ++s) {
       mbar_init(rope_full(s), kProducerWarps);
@@ -342,13 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       if (lane == 0) mbar_arrive(q_full);
     }
     if (nchunks > 1) next_valid = load(next, second_idx);
-    // This thread's 32 dims of a pair are four 16-byte columns of box part / 2.  The upper box's threads take their
-    // words in the order 2, 3, 0, 1, so the eight threads of a store phase reach eight different columns.
-    const uint32_t flip = part & 2;
-    const uint32_t dst0 = pairs + (part >> 1) * kBoxBytes + r * 128;
-    uint32_t col[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) col[i] = ((((part & 1) * 4) + (i ^ flip)) ^ (r & 7)) << 4;
+    // This thread's 64 dims of a half are the eight 16-byte columns of a row of box `part`, stored in the order
+    // i ^ 2 part, so that the eight threads of a store phase (two rows) reach eight different columns.
+    const uint32_t dst0 = pairs + part * kBoxBytes + r * 128 + (((2 * part) ^ (r & 7)) << 4);
+    const uint32_t scale_order = 0x3210u ^ (0x1111u * part);
     for (int j = 0; j < nchunks; ++j) {
       const uint32_t seen = __ballot_sync(0xFFFFFFFFu, cur_valid);
       const int rs = j % kRopeRing;
@@ -369,39 +371,35 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         reinterpret_cast<uint8_t*>(masks + j % kMaskRing)[warp] = static_cast<uint8_t>(m);
         mbar_arrive(rope_full(rs));
       }
-      // Value dims 128 q .. 128 q + 127 -> pair slot (4 j + q) mod 8, two pairs at a time: the first two are expanded in
-      // registers before their slots are free, the other two while QK^T reads the first.
+      // Value dims 256 half .. 256 half + 255 -> slot (2 j + half) mod 4: the first half is expanded in registers before its
+      // slot is free, the other while QK^T reads the first.
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint4 tile[2][4];
+      for (int half = 0; half < kHalves; ++half) {
+        // the scales of box `part` are word 4 half + part of the row's eight: with thread (4 half + part) / 2
+        const int from = (lane & ~3) + 2 * half + (part >> 1);
+        const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, cur.scales.x, from);
+        const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, cur.scales.y, from);
+        const uint32_t four = __byte_perm((part & 1) ? w1 : w0, 0, scale_order);  // in the order of the columns
+        uint32_t s[4];
+        expand_scales(four & 0xFFFFu, s[0], s[1]);
+        expand_scales(four >> 16, s[2], s[3]);
+        const uint4 a = cur.codes[half][0], b = cur.codes[half][1];
+        const bool f2 = part & 1, f4 = part & 2;
+        const uint32_t t[8] = {f2 ? a.z : a.x, f2 ? a.w : a.y, f2 ? a.x : a.z, f2 ? a.y : a.w,
+                               f2 ? b.z : b.x, f2 ? b.w : b.y, f2 ? b.x : b.z, f2 ? b.y : b.w};
+        uint4 tile[8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int q = 2 * half + i;
-          // the scales of pair q are with thread q of the row's four; this thread's two are its half word `part`
-          const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, cur.scales.x, (lane & ~3) + q);
-          const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, cur.scales.y, (lane & ~3) + q);
-          const uint32_t two = ((part & 2) ? w1 : w0) >> (16 * (part & 1));
-          uint32_t s0, s1;
-          expand_scales(two & 0xFFFFu, s0, s1);
-          const uint4 c = cur.codes[q];
-          const uint32_t sa = flip ? s1 : s0, sb = flip ? s0 : s1;
-          tile[i][0] = expand_codes(flip ? c.z : c.x, sa);
-          tile[i][1] = expand_codes(flip ? c.w : c.y, sa);
-          tile[i][2] = expand_codes(flip ? c.x : c.z, sb);
-          tile[i][3] = expand_codes(flip ? c.y : c.w, sb);
-        }
+        for (int i = 0; i < 8; ++i) tile[i] = expand_codes(f4 ? t[i ^ 4] : t[i], s[i >> 1]);
+        const int n = j * kHalves + half;
+        const int slot = n % kRing;
+        ok = ok && mbar_wait(empty(slot), static_cast<uint32_t>((n / kRing) & 1) ^ 1u, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) {
+          const uint32_t dst = dst0 + slot * kHalfBytes;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int n = j * kPairsPerChunk + 2 * half + i;
-          const int slot = n % kPairRing;
-          ok = ok && mbar_wait(pair_empty(slot), static_cast<uint32_t>((n / kPairRing) & 1) ^ 1u, abort_flag);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (ok) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) st_shared16(dst0 + slot * kPairBytes + col[k], tile[i][k]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pair_full(slot));
-          }
+          for (int i = 0; i < 8; ++i) st_shared16(dst ^ (i << 4), tile[i]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full(slot));
         }
       }
       if (!ok) break;
@@ -437,13 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         const uint32_t d = acc + kSCol + sb * kChunk;
         ok = mbar_wait(s_free(sb), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag) &&
              mbar_wait(rope_full(rs), static_cast<uint32_t>((j / kRopeRing) & 1), abort_flag);
-        // the rope box and two pairs, then the other two: few waits, and the second half overlaps its pairs' stores
-        for (int half = 0; half < 2 && ok; ++half) {
-          const int n = j * kPairsPerChunk + 2 * half;
-          const int slot = n % kPairRing;
-          const uint32_t ph = static_cast<uint32_t>((n / kPairRing) & 1);
-          ok = __all_sync(kAll, ok && mbar_wait(pair_full(slot), ph, abort_flag) &&
-                                    mbar_wait(pair_full(slot + 1), ph, abort_flag));
+        // the rope box and the first half, then the second one, whose stores overlap the first one's products
+        for (int half = 0; half < kHalves && ok; ++half) {
+          const int n = j * kHalves + half;
+          const int slot = n % kRing;
+          ok = __all_sync(kAll, ok && mbar_wait(full(slot), static_cast<uint32_t>((n / kRing) & 1), abort_flag));
           if (!ok) break;
           fence_proxy_async_smem();
           tc_fence_after();
@@ -455,10 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
                 mma_bf16(d, desc(q_lo + 8 * (kQBox >> 4) + kk * 2), desc(src + kk * 2), idesc_rope, kk > 0 ? 1u : 0u);
               mma_commit(rope_empty(rs));  // rope dims are not needed for P V
             }
-            const uint32_t src = pair_lo + slot * (kPairBytes >> 4);
+            const uint32_t src = pair_lo + slot * (kHalfBytes >> 4);
             const uint32_t qa = q_lo + 4 * half * (kQBox >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 16; ++kk)  // four steps in each of the two pairs' boxes
+            for (int kk = 0; kk < 16; ++kk)  // four steps in each of the half's boxes
               mma_bf16(d, desc(qa + (kk >> 2) * (kQBox >> 4) + (kk & 3) * 2),
                        desc(src + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2), idesc_lat, 1u);
             if (half == 1) mma_commit(s_full(sb));
@@ -478,14 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         if (elect_one()) {
           // O^T[dims 128 q ..][heads] += V^T P^T, one accumulator block per value pair
 #pragma unroll
-          for (int q = 0; q < kPairsPerChunk; ++q) {
-            const int slot = (j * kPairsPerChunk + q) % kPairRing;
-            const uint32_t v = v_lo + slot * (kPairBytes >> 4);
+          for (int q = 0; q < 2 * kHalves; ++q) {
+            const int slot = (j * kHalves + (q >> 1)) % kRing;
+            const uint32_t v = v_lo + slot * (kHalfBytes >> 4) + (q & 1) * (kPairBytes >> 4);
             const uint32_t d = acc + q * kHeads;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // A = V^T: M = 128 dims over the pair's two boxes, K = rows 16 kk ..
               mma_bf16(d, desc(v + kk * (2048 >> 4)), desc(p_lo + kk * 2), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(pair_empty(slot));
+            if (q & 1) mma_commit(empty(slot));
           }
           mma_commit(p_free);
         }

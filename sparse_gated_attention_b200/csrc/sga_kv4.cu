@@ -145,7 +145,7 @@ extern "C" {
 sga_status_t sga_kv4_append(const sga_dims_t* dims, const sga_bf16_t* kv_rows, const int32_t* q_pos, uint8_t* kv4,
                             void* ws, size_t ws_bytes, sga_stream_t stream) {
   if (!cache_dims_ok(dims)) return SGA_ERR_INVALID_ARG;
-  if (!aligned(kv_rows, 16) || !aligned(q_pos, 4) || !aligned(kv4, 16)) return SGA_ERR_INVALID_ARG;
+  if (!aligned(kv_rows, 16) || !aligned(q_pos, 4) || !aligned(kv4, 32)) return SGA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes)) return SGA_ERR_WORKSPACE;
   int sms = 0;
   const sga_status_t st = sga::host::device_info(&sms);
@@ -158,7 +158,7 @@ sga_status_t sga_kv4_append(const sga_dims_t* dims, const sga_bf16_t* kv_rows, c
 sga_status_t sga_kv4_read(const sga_dims_t* dims, const uint8_t* kv4, const int32_t* pos, sga_bf16_t* kv_rows,
                           void* ws, size_t ws_bytes, sga_stream_t stream) {
   if (!cache_dims_ok(dims)) return SGA_ERR_INVALID_ARG;
-  if (!aligned(kv_rows, 16) || !aligned(pos, 4) || !aligned(kv4, 16)) return SGA_ERR_INVALID_ARG;
+  if (!aligned(kv_rows, 16) || !aligned(pos, 4) || !aligned(kv4, 32)) return SGA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes)) return SGA_ERR_WORKSPACE;
   int sms = 0;
   const sga_status_t st = sga::host::device_info(&sms);
@@ -174,7 +174,7 @@ sga_status_t sga_sparse_mla_attend_kv4(const sga_dims_t* dims, const sga_bf16_t*
                                        const int32_t* idx, const sga_bf16_t* gate, sga_bf16_t* out, void* ws,
                                        size_t ws_bytes, sga_stream_t stream) {
   if (!attend_dims_ok(dims)) return SGA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(kv4, 16) || !aligned(idx, 16) || !aligned(out, 16) || (gate && !aligned(gate, 2)))
+  if (!aligned(q, 16) || !aligned(kv4, 32) || !aligned(idx, 16) || !aligned(out, 16) || (gate && !aligned(gate, 2)))
     return SGA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes)) return SGA_ERR_WORKSPACE;
   int sms = 0;

@@ -552,7 +552,7 @@ sga_status_t sga_layer_forward_fp8kv4(const sga_dims_t* dims, const sga_layer_fp
   if (!aligned(W->w_hq, 16) || !aligned(W->w_cq, 16) || !aligned(W->w_o, 16) || !aligned(W->w_uk, 16) ||
       !aligned(W->w_uv, 16) || !aligned(W->w_hq_scale, 4) || !aligned(W->w_cq_scale, 4) || !aligned(W->w_o_scale, 4))
     return SGA_ERR_INVALID_ARG;
-  if (!aligned(h, 16) || !aligned(q_pos, 4) || !aligned(kv4, 16) || !aligned(k_idx_cache, 16) || !aligned(y, 16) ||
+  if (!aligned(h, 16) || !aligned(q_pos, 4) || !aligned(kv4, 32) || !aligned(k_idx_cache, 16) || !aligned(y, 16) ||
       (idx_out && !aligned(idx_out, 16)))
     return SGA_ERR_INVALID_ARG;
   LayerLayout8 l;
