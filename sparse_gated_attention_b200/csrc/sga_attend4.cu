@@ -53,8 +53,9 @@ constexpr int kQPieces = kDq / 8;            // 16-byte pieces of a query head
 constexpr int kPBytes = kHeads * kChunk * 2;  // 64 heads x 64 rows fp16
 constexpr int kMaskRing = 4;
 constexpr int kProducerWarps = 8;            // warps 0-7: four threads per chunk row
-constexpr int kQkWarp = 8;                   // issues QK^T; warp 9 issues PV
-constexpr int kSoftmaxWarp = 10;             // warps 10-13
+constexpr int kQkWarp = 8;                   // warps 8 and 9 issue QK^T of every other chunk
+constexpr int kPvWarp = 10;                  // issues PV
+constexpr int kSoftmaxWarp = 11;             // warps 11-14
 constexpr int kSoftmaxThreads = 128;
 constexpr int kThreads = 32 * kSoftmaxWarp + kSoftmaxThreads;
 constexpr int kTmemCols = 512;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     mbar_init(p_full, kSoftmaxThreads / 32);
     mbar_init(p_free, 1);
     mbar_init(o_full, 1);
-    mbar_init(qk_done, 1);
+    mbar_init(qk_done, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -416,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     }
   } else if (warp < kSoftmaxWarp) {
     // ------------------------------------------------------------ MMA issuers
-    // One warp issues QK^T and one PV, each waiting on its own operands only.  The tiles, Q and P come from ordinary
+    // Two warps issue QK^T, every other chunk each, and one PV, each waiting on its own operands only: an issue lasts as
+    // long as the products, and the waits of the next chunk run meanwhile.  The tiles, Q and P come from ordinary
     // stores: they are made visible to the tensor core here, between the wait for them and the MMA (the same fence in
     // the storing warps would also wait for the rows they have in flight).  Shared-memory descriptors differ in
     // their low words only, by the address over 16 (see sdesc_sw128).
@@ -425,12 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     const auto desc_lo = [](uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); };
     const auto desc = [](uint32_t lo) { return (sdesc_sw128(0, 0, 1024) & 0xFFFFFFFF00000000ull) | lo; };
     bool ok = true;
-    if (warp == kQkWarp) {
+    if (warp < kPvWarp) {
       constexpr uint32_t idesc_lat = idesc_f16_f32(kHeads, kChunk, false, false);
       constexpr uint32_t idesc_rope = idesc_bf16_f32(kHeads, kChunk, false, false);
       const uint32_t q_lo = desc_lo(q_s, 16), pair_lo = desc_lo(pairs, 16), rope_lo = desc_lo(rope, 16);
       ok = __all_sync(kAll, mbar_wait(q_full, 0, abort_flag));
-      for (int j = 0; j < nchunks && ok; ++j) {
+      for (int j = warp - kQkWarp; j < nchunks && ok; j += 2) {
         const int sb = j & 1, rs = j % kRopeRing;
         const uint32_t d = acc + kSCol + sb * kChunk;
         ok = mbar_wait(s_free(sb), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag) &&
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
     }
-    const uint32_t done = warp == kQkWarp ? qk_done : o_full;
+    const uint32_t done = warp < kPvWarp ? qk_done : o_full;
     if (elect_one()) mma_commit(done);
     __syncwarp();
     volatile int never = 0;
