@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     for (int j = 0; j < nchunks; ++j) {
       const uint32_t seen = __ballot_sync(0xFFFFFFFFu, cur_valid);
       const int rs = j % kRopeRing;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(rope_empty(rs), static_cast<uint32_t>((j / kRopeRing) & 1) ^ 1u, abort_flag));
+      ok = mbar_wait_warp(rope_empty(rs), static_cast<uint32_t>((j / kRopeRing) & 1) ^ 1u, abort_flag);
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -393,8 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         for (int i = 0; i < 8; ++i) tile[i] = expand_codes(f4 ? t[i ^ 4] : t[i], s[i >> 1]);
         const int n = j * kHalves + half;
         const int slot = n % kRing;
-        ok = ok && mbar_wait(empty(slot), static_cast<uint32_t>((n / kRing) & 1) ^ 1u, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = ok && mbar_wait_warp(empty(slot), static_cast<uint32_t>((n / kRing) & 1) ^ 1u, abort_flag);
         if (ok) {
           const uint32_t dst = dst0 + slot * kHalfBytes;
 #pragma unroll
@@ -431,17 +430,17 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       constexpr uint32_t idesc_lat = idesc_f16_f32(kHeads, kChunk, false, false);
       constexpr uint32_t idesc_rope = idesc_bf16_f32(kHeads, kChunk, false, false);
       const uint32_t q_lo = desc_lo(q_s, 16), pair_lo = desc_lo(pairs, 16), rope_lo = desc_lo(rope, 16);
-      ok = __all_sync(kAll, mbar_wait(q_full, 0, abort_flag));
+      ok = mbar_wait_warp(q_full, 0, abort_flag);
       for (int j = warp - kQkWarp; j < nchunks && ok; j += 2) {
         const int sb = j & 1, rs = j % kRopeRing;
         const uint32_t d = acc + kSCol + sb * kChunk;
-        ok = mbar_wait(s_free(sb), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag) &&
-             mbar_wait(rope_full(rs), static_cast<uint32_t>((j / kRopeRing) & 1), abort_flag);
+        ok = mbar_wait_warp(s_free(sb), static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag) &&
+             mbar_wait_warp(rope_full(rs), static_cast<uint32_t>((j / kRopeRing) & 1), abort_flag);
         // the rope box and the first half, then the second one, whose stores overlap the first one's products
         for (int half = 0; half < kHalves && ok; ++half) {
           const int n = j * kHalves + half;
           const int slot = n % kRing;
-          ok = __all_sync(kAll, ok && mbar_wait(full(slot), static_cast<uint32_t>((n / kRing) & 1), abort_flag));
+          ok = mbar_wait_warp(full(slot), static_cast<uint32_t>((n / kRing) & 1), abort_flag);
           if (!ok) break;
           fence_proxy_async_smem();
           tc_fence_after();
@@ -469,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       constexpr uint32_t idesc_pv = idesc_f16_f32(128, kHeads, true, false);
       const uint32_t p_lo = desc_lo(p_s, 16), v_lo = desc_lo(pairs, kBoxBytes);
       for (int j = 0; j < nchunks; ++j) {
-        ok = __all_sync(kAll, mbar_wait(p_full, static_cast<uint32_t>(j & 1), abort_flag));
+        ok = mbar_wait_warp(p_full, static_cast<uint32_t>(j & 1), abort_flag);
         if (!ok) break;
         fence_proxy_async_smem();
         tc_fence_after();
@@ -512,11 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     // Every softmax thread runs every iteration, even after a wait ran out
     // (the abort flag then makes each later wait return at once), so the
     // named barriers below always see all 128 threads.
-    bool ok = mbar_wait(q_full, 0, abort_flag);
+    bool ok = mbar_wait_warp(q_full, 0, abort_flag);
     const float sc[2] = {ok ? q_scale[hrow[0]] : 0.f, ok ? q_scale[hrow[1]] : 0.f};
     for (int j = 0; j < nchunks; ++j) {
       const int sb = j & 1;
-      ok = ok && mbar_wait(s_full(sb), static_cast<uint32_t>((j >> 1) & 1), abort_flag);
+      ok = ok && mbar_wait_warp(s_full(sb), static_cast<uint32_t>((j >> 1) & 1), abort_flag);
       tc_fence_after();
       float r[32];
       tmem_ld_16x256b_x8(tmem + lane_addr + kSCol + sb * kChunk, r);
@@ -580,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         need |= !(mt[i] <= m_ref[i] + kRescaleThreshold);                       // also for a NaN
       }
       // PV_{j-1} must be done before P and O are touched.
-      ok = ok && mbar_wait(p_free, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag);
+      ok = ok && mbar_wait_warp(p_free, static_cast<uint32_t>(j & 1) ^ 1u, abort_flag);
       tc_fence_after();
       if (named_barrier_or(1, kSoftmaxThreads, need)) {
 #pragma unroll
@@ -623,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);  // P_j and any rescale of O
     }
-    ok = ok && mbar_wait(o_full, 0, abort_flag);
+    ok = ok && mbar_wait_warp(o_full, 0, abort_flag);
     if (!ok) {
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;

@@ -108,6 +108,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// mbar_wait of a whole warp: one outcome for all its threads, which keeps the code around it uniform to the compiler.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+  const long long start = clock64();
+  while (true) {
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(kAll, *abort_flag || clock64() - start > kWaitBudgetCycles)) return false;
+  }
+}
+
 // mbar_wait for warps that share their scheduler with arithmetic: each try may suspend the thread for up to 20 us (it
 // wakes when the phase completes), so a waiting warp issues next to nothing.
 __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
