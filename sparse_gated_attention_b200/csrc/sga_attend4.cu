@@ -498,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     __syncwarp();
     volatile int never = 0;
     mbar_wait(done, 0, &never);  // this warp's MMAs have finished before TMEM is read or freed
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     // As in sga_attend.cu: thread t of the warp holds rows t/4 and 8 + t/4 of its
@@ -747,16 +748,16 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
 }
 
 // Splits of the K slots of each of `rows` queries: what a wave of clusters takes, in microseconds, times their number.
-// Measured at 1 to 8 splits of 2,048 and 512 slots: 8 us beside the chunks, 1.7 us a chunk, and a merge of 4 us (5 where
-// the splits do not divide the dims evenly).  16 queries of 2,048 slots: 63.5 us unsplit, 26.5 in four, 25.4 in six, and
-// in eight, which are more clusters than run at once, 39.0.
+// Measured at 1 to 8 splits of 2,048 and 512 slots: 7.7 us beside the chunks, 1.35 us a chunk, and a merge of 3.5 us (4.5
+// where the splits do not divide the dims evenly).  16 queries of 2,048 slots: 49.7 us unsplit, 22.4 in four, 22.1 in six,
+// and in eight, which are more clusters than run at once, 33.7.
 int attend4_splits(int rows, int chunks) {
   int best = 1;
   float best_us = 0.f;
   for (int s = 1; s <= chunks && s <= kMaxSplits; ++s) {
     const int waves = (rows + host::kClusters[s - 1] - 1) / host::kClusters[s - 1];
-    const float merge = s == 1 ? 0.f : (s & (s - 1)) == 0 ? 4.2f : 5.2f;
-    const float us = static_cast<float>(waves) * (8.f + 1.7f * static_cast<float>((chunks + s - 1) / s) + merge);
+    const float merge = s == 1 ? 0.f : (s & (s - 1)) == 0 ? 3.5f : 4.5f;
+    const float us = static_cast<float>(waves) * (7.7f + 1.35f * static_cast<float>((chunks + s - 1) / s) + merge);
     if (s == 1 || us < best_us) {
       best = s;
       best_us = us;

@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     bool ok = true;
     for (int t = first; t < p.tiles && ok; t += step) {
       for (int u = u0; u < u1 && ok; ++u) {
-        ok = __all_sync(kAll, mbar_wait(full(st), ph, abort_flag) && mbar_wait(accempty(buf), aph ^ 1u, abort_flag));
+        ok = mbar_wait_warp(full(st), ph, abort_flag) && mbar_wait_warp(accempty(buf), aph ^ 1u, abort_flag);
         if (!ok) break;
         const int nkb = min(kUnit, p.k_blocks - kUnit * u);
         const uint32_t a = ring + st * Cfg::kStageBytes;
@@ -406,12 +406,12 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
       for (int kb0 = kUnit * u0; kb0 < kb_end && ok; kb0 += kChunk) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(sfull(slot), sph, abort_flag));
+        ok = mbar_wait_warp(sfull(slot), sph, abort_flag);
         if (!ok) break;
         const float* sc = scales + slot * kChunk * NP + col0;
         const int kb1 = min(kb0 + kChunk, kb_end);
         for (int kb = kb0; kb < kb1; kb += kUnit, sc += kUnit * NP) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(accfull(buf), aph, abort_flag));
+          ok = mbar_wait_warp(accfull(buf), aph, abort_flag);
           if (!ok) break;
           tc_fence_after();
           // both K blocks of the unit (the second one's columns go unused past the last K block)
