@@ -12,7 +12,7 @@
 //   * A code times its scale has at most 6 significant bits between 2^-10 and
 //     2,688, so it is exact in fp16 (and in bf16).  The tiles hold fp16: two
 //     codes expand with one conversion and one multiplication, and P can be one
-//     fp16 operand (half a step is 2^-12, an eighth of the rounding of the bf16
+//     fp16 operand (half a step is 2^-11, an eighth of the rounding of the bf16
 //     result) where the bf16 kernel needs two bf16 parts: half the PV
 //     instructions.
 //   * Q must then be fp16 for the latent dims.  Each head is scaled by the power
@@ -20,10 +20,19 @@
 //     its 8 bits exactly down to 2^-31 of the head's largest, and the factor
 //     is taken out again in the softmax scale.  The rope dims stay bf16 on both
 //     sides (kind::f16 takes either type, one per instruction).
-// Everything else is as there: one CTA per (query, split), the splits of a query
-// a cluster; QK^T with M = 64 heads, N = 64 rows; PV transposed, O^T [512 x 64] in
-// tensor memory; a lazy running maximum in the log2 domain; the splits merged
-// through distributed shared memory.
+// Otherwise as there: one CTA per (query, split), the splits of a query a cluster;
+// QK^T with M = 64 heads, N = 64 rows; PV transposed, O^T [512 x 64] in tensor
+// memory; a lazy running maximum in the log2 domain; the splits merged through
+// distributed shared memory.
+//
+// Bound by the shared memory's 128 bytes a cycle: a chunk's products read 240 KB of
+// operands (1,900 cycles), its tiles and P are 72 KB of stores, and a chunk takes
+// 2,600 cycles.  512 queries of 2,048 slots: 201 us (146 GFLOP, 0.73 PFLOP/s).  Few queries
+// are bound by the chain of one chunk after another and by the merge (128 KB per CTA
+// over the distributed shared memory, 19 bytes a cycle): 4 queries 16.2 us, 32 queries
+// over 32,768 positions 27.3 us.  Measured and left out: eight softmax warps (a
+// wave of 148 queries 78 us against 52), two groups of them by turns (a fifth slower),
+// waits by one lane of a warp (84 us), loads predicated and not branched around (56 us).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -310,12 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     RowPart cur, next;
     bool cur_valid, next_valid = false;
     {
-      // Q: four threads per head, 16-byte pieces part, part + 4, ...; pieces 64.. are the rope dims
+      // Q: four threads per head, 16-byte pieces part, part + 4, ...; pieces 64.. are the rope dims.  Odd heads take them in
+      // pairs the other way round, so that the eight threads of a store phase (two heads) reach eight different columns.
       const int h = r;
       const uint8_t* q_row = reinterpret_cast<const uint8_t*>(p.q) + (static_cast<size_t>(row) * kHeads + h) * kDq * 2;
       uint4 v[kQPieces / 4];
 #pragma unroll
-      for (int i = 0; i < kQPieces / 4; ++i) v[i] = ld_row16(q_row + 16 * (part + 4 * i));
+      for (int i = 0; i < kQPieces / 4; ++i) v[i] = ld_row16(q_row + 16 * (part + 4 * (i ^ (h & 1))));
       cur_valid = load(cur, first_idx);
       uint32_t top = 0;  // largest magnitude as bf16 bits
 #pragma unroll
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
       for (int i = 0; i < kQPieces / 4; ++i) {
-        const int c = part + 4 * i;
+        const int c = part + 4 * (i ^ (h & 1));
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         uint32_t o[4];
 #pragma unroll
@@ -639,24 +649,19 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     }
   }
 
-  // ---- split merge, as in sga_attend.cu: out = g / L * sum_r 2^(m_r - M) O_r with
-  // M = max_r m_r and L = sum_r 2^(m_r - M) l_r (per head).  Every thread of the
-  // cluster takes part in its barriers, on every path.
+  // ---- split merge: out = g / L * sum_r 2^(m_r - M) O_r with M = max_r m_r and L = sum_r 2^(m_r - M) l_r (per head).
+  // Every thread of the cluster takes part in its barriers, on every path.
   const int S = p.splits;
-  float* o_stage = reinterpret_cast<float*>(smem);  // value ring + rope slots + Q buffer, idle after the MMAs
+  float* recv = reinterpret_cast<float*>(smem);          // value ring + rope slots + Q buffer, idle after the MMAs
+  float* weight = reinterpret_cast<float*>(p_ptr);       // [S][64] the splits' factors, over P
+  // One thread a head works out the factors: in a cluster one of the issuing warps, while the others send.
+  const int head = warp * 32 + lane - kQkWarp * 32;
+  const bool weighs = warp >= kQkWarp && warp < kQkWarp + 2;
+  float g = 1.f;
+  if (weighs && p.gate) g = sigmoidf_(bf16_bits_to_float(p.gate[static_cast<size_t>(row) * kHeads + head]));
   if (S > 1) {
     cluster.sync();  // every split's (m, l) published; all MMAs of every CTA done
-  } else {
-    __syncthreads();
-  }
-  if (warp >= kSoftmaxWarp && lane < 16) {
-    const int head = (warp & 3) * 16 + lane;
-    const float g = p.gate ? sigmoidf_(bf16_bits_to_float(p.gate[static_cast<size_t>(row) * kHeads + head])) : 1.f;
-    float f;
-    if (S == 1) {
-      const float l = own_ml[head].y;
-      f = l == 0.f ? 0.f : g / l;
-    } else {
+    if (weighs) {
       // every split's (m, l) for this head, all loads in flight at once
       float2 ml[kMaxSplits];
 #pragma unroll
@@ -667,19 +672,27 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       for (int r = 0; r < kMaxSplits; ++r) mx = fmaxf(mx, ml[r].x);
       float L = 0.f;
 #pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r) {
+        ml[r].x = ml[r].x == -INFINITY ? 0.f : exp2f(ml[r].x - mx);
+        L += ml[r].x * ml[r].y;
+      }
+      const float f = L == 0.f ? 0.f : g / L;
+#pragma unroll
       for (int r = 0; r < kMaxSplits; ++r)
-        if (ml[r].x != -INFINITY) L += exp2f(ml[r].x - mx) * ml[r].y;
-      const float m_own = own_ml[head].x;
-      f = (L != 0.f && m_own != -INFINITY) ? exp2f(m_own - mx) * g / L : 0.f;
+        if (r < S) weight[r * kHeads + head] = ml[r].x * f;
     }
-    head_f[head] = f;
+  } else {
+    __syncthreads();
+    if (weighs) {
+      const float l = own_ml[head].y;
+      weight[head] = l == 0.f ? 0.f : g / l;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   // With several splits, CTA r owns the float4 columns [v0(r), v0(r+1)) of
-  // every head's 512 dims, v0(r) = 128 r / S; every CTA pushes its scaled O for
+  // every head's 512 dims, v0(r) = 128 r / S; every CTA pushes its O for
   // those dims into the owner's receive buffer [source split][head][kStride].
   const int kStride = 4 * ((kDv / 4 + S - 1) / S);  // floats per (source, head) row: the widest slice
-  float* recv = o_stage;
   if (warp < kProducerWarps || warp >= kSoftmaxWarp) {
     // Twelve warps read O^T out of TMEM: warp w reads lane quarter w % 4; the
     // producer warps 0-3 take dim block 0, 4-7 block 1, the softmax warps blocks 2-3.
@@ -690,9 +703,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     const int blk1 = warp < kProducerWarps ? blk0 + 1 : 4;
     tc_fence_after();
     for (int c = 0; c < 2; ++c) {
-      float hf[32];
+      float f[32];  // the unsplit query's factors
+      if (S == 1) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) hf[i] = head_f[c * 32 + i];
+        for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(weight + c * 32 + i);
+      }
       for (int blk = blk0; blk < blk1; ++blk) {
         const int dim = 128 * blk + 32 * quarter + lane;
         float o[32];
@@ -703,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
                           static_cast<size_t>(c * 32 + (lane & 1)) * kDv + (dim & ~1);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float a = o[i] * hf[i], b = o[i + 1] * hf[i + 1];
+            const float a = o[i] * f[i], b = o[i + 1] * f[i + 1];
             const float got = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : b, 1);
             *reinterpret_cast<uint32_t*>(col + static_cast<size_t>(i) * kDv) =
                 lane & 1 ? pack_bf16(got, b) : pack_bf16(a, got);
@@ -714,13 +729,13 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
           const int dl = dim - 4 * ((kDv / 4) * owner / S);
           float* col = cluster.map_shared_rank(recv + (split * kHeads + c * 32) * kStride + dl, owner);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) col[i * kStride] = o[i] * hf[i];
+          for (int i = 0; i < 32; ++i) col[i * kStride] = o[i];
         }
       }
     }
   }
   if (S > 1) {
-    cluster.sync();  // every split's scaled O delivered to its owners
+    cluster.sync();  // every split's O delivered to its owners, and the weights written
     const int v0 = (kDv / 4) * split / S, v1 = (kDv / 4) * (split + 1) / S;
     const int vecs = v1 - v0;
     uint16_t* orow = p.out + static_cast<size_t>(row) * kHeads * kDv;
@@ -729,10 +744,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int r = 0; r < S; ++r) {
         const float4 x = *reinterpret_cast<const float4*>(recv + (r * kHeads + h) * kStride + 4 * dv);
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+        const float f = weight[r * kHeads + h];
+        acc.x = fmaf(x.x, f, acc.x);
+        acc.y = fmaf(x.y, f, acc.y);
+        acc.z = fmaf(x.z, f, acc.z);
+        acc.w = fmaf(x.w, f, acc.w);
       }
       *reinterpret_cast<uint2*>(orow + h * kDv + 4 * (v0 + dv)) =
           make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
