@@ -278,7 +278,7 @@ SGA_API sga_status_t sga_forward_kv4(const sga_dims_t* dims, const sga_bf16_t* q
  * as the largest bf16 and becomes +-448; a NaN stays a NaN and does not count.
  *   x [rows][cols] bf16    codes [rows][cols] E4M3 bytes
  *   scale [rows][ceil(cols / 128)] fp32
- * cols is a multiple of 16; x and codes 16-byte aligned. */
+ * cols is a multiple of 16, at most 2^30; x and codes 16-byte aligned. */
 SGA_API sga_status_t sga_quantize_fp8(int32_t rows, int32_t cols, const sga_bf16_t* x, sga_fp8_e4m3_t* codes,
                                       float* scale, sga_stream_t stream);
 
@@ -294,7 +294,8 @@ typedef enum { SGA_OUT_FP32 = 0, SGA_OUT_BF16 = 1 } sga_out_type_t;
  * the tensor core, the scaled blocks in fp32 in a fixed order (results do not
  * depend on the schedule); a bf16 y is rounded once.  k is a multiple of 16; x
  * and w 16-byte aligned, y aligned to its elements.  The last blocks may be
- * partial.  Workspace: the status word only, 256 bytes. */
+ * partial.  n, m and k are at most 2^30 each.  Workspace: the status word only,
+ * 256 bytes; calls on several streams may share it. */
 SGA_API sga_status_t sga_gemm_fp8(int32_t n, int32_t m, int32_t k, const sga_fp8_e4m3_t* x, const float* x_scale,
                                   const sga_fp8_e4m3_t* w, const float* w_scale, void* y, sga_out_type_t out_type,
                                   void* ws, size_t ws_bytes, sga_stream_t stream);

@@ -37,6 +37,7 @@ namespace sga {
 namespace {
 
 constexpr int kBlock = 128;  // K elements (bytes) and weight rows that share a scale
+constexpr int kMaxExtent = 1 << 30;  // of any dimension: the last tile's end stays within an int
 
 // ---------------------------------------------------------------- quantiser
 constexpr int kQuantLanes = 16;  // threads per block of 128: 8 values (16 bytes) each
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         uint32_t ph = 0, aph = 0;
         bool ok = true;
         for (long long i = buf; i < blocks; i += 2) {
-          ok = __all_sync(kAll, mbar_wait_idle(full(st), ph, abort_flag) && mbar_wait_idle(accempty(buf), aph ^ 1u, abort_flag));
+          ok = mbar_wait_idle_warp(full(st), ph, abort_flag) && mbar_wait_idle_warp(accempty(buf), aph ^ 1u, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -821,7 +822,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
       for (int i = 0; i < kBlock; ++i) acc[i] = 0.f;
       for (int kb0 = 0; kb0 < p.k_blocks && ok; kb0 += kTChunk) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_idle(sfull(slot), sph, abort_flag));
+        ok = mbar_wait_idle_warp(sfull(slot), sph, abort_flag);
         if (!ok) break;
         const float* sc = scales + slot * kTScaleFloats;
         const int kbs = min(kTChunk, p.k_blocks - kb0);
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         for (int kbl = 0; kbl < kbs; ++kbl) {
           const float s = s_next;
           if (kbl + 1 < kbs) s_next = sc[(kbl + 1) * kTScaleLd + tok] * sc[kTChunk * kTScaleLd + half * kTChunk + kbl + 1];
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_idle(accfull(buf), aph, abort_flag));
+          ok = mbar_wait_idle_warp(accfull(buf), aph, abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -963,13 +964,13 @@ cudaError_t launch_gemm_fp8(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   if (a.n <= 32) return launch_stream<32>(a, num_sms, s);
   if (a.n <= 64) return launch_stream<64>(a, num_sms, s);
   // More tokens: blocks of 128 through the streaming kernel, whose split K or smaller tiles fill the SMs where there are
-  // few, or tiles of 256 x 256, which read the operands less often (a K block 0.47 us, another tile's output 5 us).
-  // n x m x k, streaming against tiles: 256 x 2304 x 7168 16.0 us against 34.6, 512 x 4096 x 4096 17.7 against 23.4;
-  // 700 x 4096 x 4096 31.9 against 24.1, 400 x 7168 x 8192 58.6 against 39.9.
+  // few, or tiles of 256 x 256, which read the operands less often (a K block 0.45 us, another tile's output 5 us).
+  // n x m x k, streaming against tiles: 256 x 2304 x 7168 15.6 us against 33, 512 x 4096 x 4096 17.7 against 21.5;
+  // 700 x 4096 x 4096 31.9 against 21.5, 400 x 7168 x 8192 58.6 against 37.
   const long long k_blocks = (a.k + kBlock - 1) / kBlock;
   const long long m128 = (a.m + kTileM - 1) / kTileM, n128 = (a.n + 127) / 128;
   const long long waves = (((a.m + kTN - 1) / kTN) * static_cast<long long>((a.n + 2 * kTM - 1) / (2 * kTM)) + 73) / 74;
-  const float tile_us = 7.f + 0.47f * static_cast<float>(k_blocks * waves) + 5.f * static_cast<float>(waves - 1);
+  const float tile_us = 7.f + 0.45f * static_cast<float>(k_blocks * waves) + 5.f * static_cast<float>(waves - 1);
   if (stream_plan(128, m128 * n128, static_cast<int>((k_blocks + kUnit - 1) / kUnit)).us < tile_us)
     return launch_stream<128>(a, num_sms, s);
   return launch_tile(a, num_sms, s);
@@ -982,7 +983,7 @@ extern "C" {
 sga_status_t sga_quantize_fp8(int32_t rows, int32_t cols, const sga_bf16_t* x, sga_fp8_e4m3_t* codes, float* scale,
                               sga_stream_t stream) {
   using sga::host::aligned;
-  if (rows < 1 || cols < 16 || cols % 16 != 0) return SGA_ERR_INVALID_ARG;
+  if (rows < 1 || cols < 16 || cols % 16 != 0 || cols > sga::kMaxExtent) return SGA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return SGA_ERR_INVALID_ARG;
   int sms = 0;
   const sga_status_t st = sga::host::device_info(&sms);
@@ -997,6 +998,7 @@ sga_status_t sga_gemm_fp8(int32_t n, int32_t m, int32_t k, const sga_fp8_e4m3_t*
                           size_t ws_bytes, sga_stream_t stream) {
   using sga::host::aligned;
   if (n < 1 || m < 1 || k < 16 || k % 16 != 0) return SGA_ERR_INVALID_ARG;
+  if (n > sga::kMaxExtent || m > sga::kMaxExtent || k > sga::kMaxExtent) return SGA_ERR_INVALID_ARG;
   if (out_type != SGA_OUT_FP32 && out_type != SGA_OUT_BF16) return SGA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(x_scale, 4) || !aligned(w, 16) || !aligned(w_scale, 4) ||
       !aligned(y, out_type == SGA_OUT_FP32 ? 4 : 2))

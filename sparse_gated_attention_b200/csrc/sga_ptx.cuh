@@ -139,6 +139,25 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, vo
   }
 }
 
+// mbar_wait_idle of a whole warp, with one outcome (see mbar_wait_warp).
+__device__ __forceinline__ bool mbar_wait_idle_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  long long start = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000)
+        : "memory");
+    if (__all_sync(kAll, ok)) return true;
+    if (start == 0) start = clock64();
+    if (__any_sync(kAll, *abort_flag || clock64() - start > kWaitBudgetCycles)) return false;
+  }
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {

@@ -513,13 +513,13 @@ def test_two_streams_at_once():
     want = [sga.gemm_fp8(*c) for c in cases]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in cases]
-    spaces = [status_ws() for _ in cases]
+    ws = status_ws()
     torch.cuda.synchronize()
     outs = [[], []]
     for _ in range(10):
         for i, s in enumerate(streams):
             with torch.cuda.stream(s):
-                outs[i].append(sga.gemm_fp8(*cases[i], ws=spaces[i]))
+                outs[i].append(sga.gemm_fp8(*cases[i], ws=ws))
     torch.cuda.synchronize()
     for i in range(2):
         for y in outs[i]:

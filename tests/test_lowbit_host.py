@@ -87,6 +87,10 @@ def test_kv4_calls_refuse_bad_arguments(lib):
     assert lib.sga_kv4_append(r, GOOD, GOOD, GOOD, P(0x20000010), 256, None) == 3
     assert lib.sga_kv4_append(r, GOOD, GOOD, GOOD, WS, 255, None) == 3
     assert lib.sga_kv4_append(None, GOOD, GOOD, GOOD, WS, 256, None) == 1
+    half = P(0x100010)  # a cache row is read 32 bytes at a time
+    assert lib.sga_kv4_append(r, GOOD, GOOD, half, WS, 256, None) == 1
+    assert lib.sga_kv4_read(r, half, GOOD, GOOD, WS, 256, None) == 1
+    assert lib.sga_sparse_mla_attend_kv4(r, GOOD, half, GOOD, None, GOOD, WS, 256, None) == 1
     assert lib.sga_kv4_read(r, GOOD, None, GOOD, WS, 256, None) == 1
     assert lib.sga_kv4_read(r, GOOD, GOOD, ODD, WS, 256, None) == 1
     assert lib.sga_sparse_mla_attend_kv4(r, GOOD, None, GOOD, None, GOOD, WS, 256, None) == 1
@@ -119,6 +123,7 @@ def test_attend_kv4_refuses_bad_top_k(lib, top_k):
 def test_quantize_refuses_bad_arguments(lib):
     for rows, cols in [(0, 16), (1, 0), (1, 15), (1, 24), (-1, 16)]:
         assert lib.sga_quantize_fp8(rows, cols, GOOD, GOOD, GOOD, None) == 1
+    assert lib.sga_quantize_fp8(1, 2**31 - 16, GOOD, GOOD, GOOD, None) == 1
     assert lib.sga_quantize_fp8(1, 16, ODD, GOOD, GOOD, None) == 1
     assert lib.sga_quantize_fp8(1, 16, GOOD, P(0x100008), GOOD, None) == 1
     assert lib.sga_quantize_fp8(1, 16, GOOD, GOOD, None, None) == 1
@@ -129,7 +134,8 @@ def test_product_refuses_bad_arguments(lib):
     def call(n=4, m=5, k=32, x=GOOD, xs=GOOD, w=GOOD, wsc=GOOD, y=GOOD, t=0, ws=WS, nbytes=256):
         return lib.sga_gemm_fp8(n, m, k, x, xs, w, wsc, y, t, ws, nbytes, None)
 
-    for bad in [dict(n=0), dict(m=0), dict(k=0), dict(k=24), dict(n=-3), dict(t=2), dict(x=None), dict(x=ODD),
+    top = 2**31 - 1
+    for bad in [dict(n=0), dict(m=0), dict(k=0), dict(k=24), dict(n=-3), dict(n=top), dict(m=top), dict(k=top - 15), dict(t=2), dict(x=None), dict(x=ODD),
                 dict(w=ODD), dict(xs=ODD), dict(wsc=None), dict(y=None), dict(y=ODD), dict(y=P(0x100001), t=1)]:
         assert call(**bad) == 1, bad
     for bad in [dict(ws=None), dict(ws=P(0x20000010)), dict(nbytes=255)]:
