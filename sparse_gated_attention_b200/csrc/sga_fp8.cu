@@ -15,11 +15,11 @@
 // Where the tiles do not fill the SMs, K is split over a cluster whose thread blocks add up each other's partial sums
 // through distributed shared memory, in a fixed order: the result does not depend on the schedule, and no second launch is
 // needed.  (Sums in global memory by whichever block arrived last cost 4 to 6 us more.)  4 x 2304 x 7168 (n x m x k)
-// 7.0 us, 2.4 TB/s; 32 x 20544 x 1536 8.8 us, 3.8 TB/s; 256 x 2304 x 7168 16.0 us.
+// 7.0 us, 2.4 TB/s; 32 x 20544 x 1536 8.6 us, 3.8 TB/s; 256 x 2304 x 7168 15.6 us.
 //
 // gemm_fp8_tile_kernel, many tokens: pairs of CTAs, 256 tokens x 256 channels a tile, the tokens as M.  Bound by the
 // hand-over between the MMA (512 cycles a K block) and the scaled sums in registers (450 cycles) over two accumulators of
-// 256 columns, and by power at large sizes: 4096 x 7168 x 8192 253 us on zeros, 291 on data, 1.65 PFLOP/s (the MMAs alone
+// 256 columns, and by power at large sizes: 4096 x 7168 x 8192 227 us on zeros, 264 on data, 1.8 PFLOP/s (the MMAs alone
 // 147).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
