@@ -27,10 +27,10 @@
 //
 // Bound by the shared memory's 128 bytes a cycle: a chunk's products read 240 KB of
 // operands (1,900 cycles), its tiles and P are 72 KB of stores, and a chunk takes
-// 2,600 cycles.  512 queries of 2,048 slots: 201 us (146 GFLOP, 0.73 PFLOP/s).  Few queries
+// 2,600 cycles.  512 queries of 2,048 slots: 198 us (146 GFLOP, 0.74 PFLOP/s).  Few queries
 // are bound by the chain of one chunk after another and by the merge (128 KB per CTA
-// over the distributed shared memory, 19 bytes a cycle): 4 queries 16.2 us, 32 queries
-// over 32,768 positions 27.3 us.  Measured and left out: eight softmax warps (a
+// over the distributed shared memory, 19 bytes a cycle): 4 queries 15.9 us, 32 queries
+// over 32,768 positions 26.2 us.  Measured and left out: eight softmax warps (a
 // wave of 148 queries 78 us against 52), two groups of them by turns (a fifth slower),
 // waits by one lane of a warp (84 us), loads predicated and not branched around (56 us).
 #include <cooperative_groups.h>
@@ -58,7 +58,6 @@ constexpr int kRing = 2 * kHalves;           // two chunks of value tiles
 constexpr int kRopeRing = 2;
 constexpr int kQBox = kHeads * 128;          // 64 heads x 64 dims
 constexpr int kQBytes = 9 * kQBox;
-constexpr int kQPieces = kDq / 8;            // 16-byte pieces of a query head
 constexpr int kPBytes = kHeads * kChunk * 2;  // 64 heads x 64 rows fp16
 constexpr int kMaskRing = 4;
 constexpr int kProducerWarps = 8;            // warps 0-7: four threads per chunk row
@@ -223,6 +222,46 @@ __device__ __forceinline__ void load_row(RowPart& d, const uint8_t* row, int par
   }
 }
 
+// The part of a query head that one of eight threads converts: column `part` of the head's row in the nine boxes.
+struct QPart {
+  uint4 v[9];
+};
+
+__device__ __forceinline__ void load_q(QPart& d, const uint16_t* q, int row, int head, int part) {
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(q) + (static_cast<size_t>(row) * kHeads + head) * kDq * 2 + 16 * part;
+#pragma unroll
+  for (int i = 0; i < 9; ++i) d.v[i] = ld_row16(src + 128 * i);
+}
+
+__device__ __forceinline__ void store_q(const QPart& d, uint32_t q_s, float* q_scale, int head, int part, float scale_log2) {
+  uint32_t top = 0;  // largest magnitude as bf16 bits
+#pragma unroll
+  for (int i = 0; i < 9; ++i) {
+    const uint32_t w[4] = {d.v[i].x, d.v[i].y, d.v[i].z, d.v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  // 2^e takes a largest value of exponent x to exponent 14; heads smaller than 2^-86 have logits of zero anyway
+  int e = 14 + 127 - static_cast<int>(top >> 7);
+  e = top == 0 ? 0 : min(max(e, -113), 100);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+  for (int i = 0; i < 9; ++i) {
+    const uint32_t w[4] = {d.v[i].x, d.v[i].y, d.v[i].z, d.v[i].w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = __uint_as_float(w[k] << 16) * up, hi = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+      o[k] = i < kDv / 64 ? pack_f16(lo, hi) : pack_bf16(lo, hi);  // the last box holds the rope dims
+    }
+    st_shared16(q_s + i * kQBox + head * 128 + ((part ^ (head & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+  }
+  if (part == 0) q_scale[head] = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
 __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -269,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
       mbar_init(rope_full(s), kProducerWarps);
       mbar_init(rope_empty(s), 1);
     }
-    mbar_init(q_full, kProducerWarps);
+    mbar_init(q_full, kProducerWarps + kSoftmaxThreads / 32);
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(s_free(b), kSoftmaxThreads / 32);
@@ -319,41 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     RowPart cur, next;
     bool cur_valid, next_valid = false;
     {
-      // Q: four threads per head, 16-byte pieces part, part + 4, ...; pieces 64.. are the rope dims.  Odd heads take them in
-      // pairs the other way round, so that the eight threads of a store phase (two heads) reach eight different columns.
-      const int h = r;
-      const uint8_t* q_row = reinterpret_cast<const uint8_t*>(p.q) + (static_cast<size_t>(row) * kHeads + h) * kDq * 2;
-      uint4 v[kQPieces / 4];
-#pragma unroll
-      for (int i = 0; i < kQPieces / 4; ++i) v[i] = ld_row16(q_row + 16 * (part + 4 * (i ^ (h & 1))));
+      // Q: this warp's four of the heads 0-31 (the softmax warps take the others)
+      QPart v;
+      load_q(v, p.q, row, 4 * warp + (lane >> 3), lane & 7);
       cur_valid = load(cur, first_idx);
-      uint32_t top = 0;  // largest magnitude as bf16 bits
-#pragma unroll
-      for (int i = 0; i < kQPieces / 4; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
-      }
-      top = max(top & 0xFFFFu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      // 2^e takes a largest value of exponent x to exponent 14; heads smaller than 2^-86 have logits of zero anyway
-      int e = 14 + 127 - static_cast<int>(top >> 7);
-      e = top == 0 ? 0 : min(max(e, -113), 100);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-      for (int i = 0; i < kQPieces / 4; ++i) {
-        const int c = part + 4 * (i ^ (h & 1));
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float lo = __uint_as_float(w[k] << 16) * up, hi = __uint_as_float(w[k] & 0xFFFF0000u) * up;
-          o[k] = i < kDv / 32 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-        }
-        st_shared16(q_s + (c >> 3) * kQBox + h * 128 + (((c & 7) ^ (h & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-      }
-      if (part == 0) q_scale[h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      store_q(v, q_s, q_scale, 4 * warp + (lane >> 3), lane & 7, p.scale_log2);
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
@@ -522,6 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     // Every softmax thread runs every iteration, even after a wait ran out
     // (the abort flag then makes each later wait return at once), so the
     // named barriers below always see all 128 threads.
+    {
+      // Q: this warp's eight of the heads 32-63
+      QPart v[2];
+      const int head = 32 + 8 * (warp - kSoftmaxWarp) + (lane >> 3);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_q(v[i], p.q, row, head + 4 * i, lane & 7);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) store_q(v[i], q_s, q_scale, head + 4 * i, lane & 7, p.scale_log2);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
     bool ok = mbar_wait_warp(q_full, 0, abort_flag);
     const float sc[2] = {ok ? q_scale[hrow[0]] : 0.f, ok ? q_scale[hrow[1]] : 0.f};
     for (int j = 0; j < nchunks; ++j) {
@@ -608,15 +628,17 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
         weights();
         if (j > 0) {
           named_barrier(1, kSoftmaxThreads);
-          // O^T[dim][head] *= alpha[head]: every lane holds one dim of each block
-          for (int blk = 0; blk < 4; ++blk) {
-            for (int c = 0; c < 2; ++c) {
-              float o[32];
-              tmem_ld32(tmem + lane_addr + blk * kHeads + c * 32, o);
+          // O^T[dim][head] *= alpha[head], 32 heads of a block at a time: every lane holds one dim of each block.  Not
+          // unrolled, or the registers that takes are spilled elsewhere.
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            float o[32];
+            const uint32_t src = tmem + lane_addr + c * 32;
+            const float* f = head_f + (c & 1) * 32;
+            tmem_ld32(src, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= head_f[c * 32 + i];
-              tmem_st32(tmem + lane_addr + blk * kHeads + c * 32, o);
-            }
+            for (int i = 0; i < 32; ++i) o[i] *= f[i];
+            tmem_st32(src, o);
           }
           named_barrier(1, kSoftmaxThreads);
         }
