@@ -844,7 +844,7 @@ cudaError_t launch_attend4(const Attend4Args& a, cudaStream_t stream) {
   p.chunks = a.top_k / kChunk;
   p.scale_log2 = static_cast<float>(SGA_SOFTMAX_SCALE * 1.4426950408889634);
   // Full waves of whole queries, then the rest with its slots split over the SMs it would leave idle: 512 queries of
-  // 2,048 slots (3.46 waves) 248 us against 274 in one launch.
+  // 2,048 slots (3.46 waves) 198 us against 215 in one launch.
   const int tail = rows % host::kClusters[0];
   const int tail_splits = tail ? attend4_splits(tail, p.chunks) : 1;
   const int whole = tail_splits > 1 ? rows - tail : rows;

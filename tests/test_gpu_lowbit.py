@@ -142,13 +142,22 @@ PRODUCT_SHAPES = [(1, 1, 16), (1, 128, 128), (2, 129, 144), (16, 64, 4112), (17,
                   (33, 1000, 1552), (64, 256, 512), (65, 130, 656), (127, 384, 1536), (129, 257, 400),
                   (333, 1111, 1552), (512, 640, 2048), (1000, 300, 144),
                   # tiles of 256 x 256: odd output rows, one wave and several, a short last tile each way
-                  (700, 2304, 272), (2000, 1111, 272), (400, 7168, 1024), (2300, 4000, 400)]
+                  (700, 2304, 272), (2000, 1111, 272), (400, 7168, 1024), (2300, 4000, 400), (1100, 2049, 528),
+                  (2100, 5001, 1040), (2100, 5002, 1040)]
 
 
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("n,m,k", PRODUCT_SHAPES)
 def test_product_matches_definition(n, m, k, out_dtype):
     check_product(n, m, k, out_dtype, seed=n + m + k)
+
+
+@pytest.mark.parametrize("n", [9, 30, 50, 100])
+@pytest.mark.parametrize("m,units", [(77, 2), (77, 6), (77, 7), (77, 9), (77, 10), (77, 11), (77, 13), (77, 17), (77, 21),
+                                     (77, 31), (5800, 6), (5800, 8)])
+def test_product_with_k_in_one_to_eight_parts(n, m, units):
+    """K of that many pairs of blocks, the last one partial: the split grows with it, from none to eight."""
+    check_product(n, m, 256 * units - 112, torch.bfloat16, seed=units)
 
 
 @pytest.mark.parametrize("n,m,k", [(1, 7168, 8192), (4, 130, 20000), (40, 300, 1680), (300, 513, 1040),
