@@ -786,16 +786,16 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
 }
 
 // Splits of the K slots of each of `rows` queries: what a wave of clusters takes, in microseconds, times their number.
-// Measured at 1 to 8 splits of 2,048 and 512 slots: 7.7 us beside the chunks, 1.35 us a chunk, and a merge of 3.5 us (4.5
-// where the splits do not divide the dims evenly).  16 queries of 2,048 slots: 49.7 us unsplit, 22.4 in four, 22.1 in six,
-// and in eight, which are more clusters than run at once, 33.7.
+// Measured at 1 to 8 splits of 2,048 and 512 slots: 6.7 us beside the chunks, 1.3 us a chunk, and a merge of 3.6 us (4.6
+// where the splits do not divide the dims evenly).  16 queries of 2,048 slots: 48.9 us unsplit, 21.8 in four, 21.1 in six,
+// and in eight, which are more clusters than run at once, 31.8.
 int attend4_splits(int rows, int chunks) {
   int best = 1;
   float best_us = 0.f;
   for (int s = 1; s <= chunks && s <= kMaxSplits; ++s) {
     const int waves = (rows + host::kClusters[s - 1] - 1) / host::kClusters[s - 1];
-    const float merge = s == 1 ? 0.f : (s & (s - 1)) == 0 ? 3.5f : 4.5f;
-    const float us = static_cast<float>(waves) * (7.7f + 1.35f * static_cast<float>((chunks + s - 1) / s) + merge);
+    const float merge = s == 1 ? 0.f : (s & (s - 1)) == 0 ? 3.6f : 4.6f;
+    const float us = static_cast<float>(waves) * (6.7f + 1.31f * static_cast<float>((chunks + s - 1) / s) + merge);
     if (s == 1 || us < best_us) {
       best = s;
       best_us = us;
