@@ -600,6 +600,7 @@ struct TileParams {
   float* out_f32;
   uint16_t* out_bf16;
   int* status;
+  bool pair_stores;  // every even channel of out_bf16 lies on a 4-byte boundary
 };
 
 // (a, b) += (x, y) * s, two lanes an instruction.
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         for (int i = 0; i < 32; ++i) stage[lane * 33 + i] = acc[c + i];
         __syncwarp();
         const int ch = ch0 + c + lane;
-        if (p.out_bf16 && (p.m & 1) == 0) {  // two tokens a store, two channels a lane
+        if (p.pair_stores) {  // two tokens a store, two channels a lane
           const int pair_ch = ch0 + c + 2 * (lane & 15);
           uint16_t* o = p.out_bf16 + static_cast<size_t>(token0 + (lane >> 4)) * p.m + pair_ch;
 #pragma unroll 8
@@ -920,6 +921,7 @@ cudaError_t launch_tile(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   p.out_f32 = a.out_f32;
   p.out_bf16 = a.out_bf16;
   p.status = a.status;
+  p.pair_stores = host::aligned(a.out_bf16, 4) && a.m % 2 == 0;
   CUtensorMap wmap, xmap;
   cudaError_t e = make_tmap_2d(&wmap, true, a.w, a.k, a.m, a.k, kBlock, kTN / 2);
   if (e != cudaSuccess) return e;

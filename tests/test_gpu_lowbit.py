@@ -209,6 +209,20 @@ def test_product_leading_dims_and_out():
     assert got is out and torch.equal(out.view(6, 96), want)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,m,k", [(20, 130, 272), (100, 130, 272), (2000, 2304, 528), (2000, 2303, 528)])
+def test_product_writes_from_any_element_on(n, m, k, out_dtype):
+    """The output is a view that starts one element into its storage: with an even m, no row of a bf16 output lies on a
+    4-byte boundary.  Few tokens, many, and many with rows of both parities; the elements around the view stay."""
+    case = product_case(n, m, k, n + m)
+    want = sga.gemm_fp8(*case, out_dtype=out_dtype)
+    room = torch.full((n * m + 2,), 7.0, dtype=out_dtype, device=DEV)
+    out = room[1:-1].view(n, m)
+    assert out.data_ptr() % (2 * out.element_size()) != 0
+    assert sga.gemm_fp8(*case, out=out) is out
+    assert torch.equal(out, want) and room[0] == 7 and room[-1] == 7
+
+
 # ------------------------------------------------------------------------------------------------ 4-bit cache rows
 def check_append(rows, pos, L):
     B, T = pos.shape
