@@ -3,6 +3,7 @@
 Every step of the path runs in the CUDA library; this module checks tensor
 shapes, dtypes and devices, allocates outputs and workspaces with PyTorch when
 the caller does not pass them, and forwards raw pointers and the current CUDA
+stream, or the one given as `stream`: what a call allocates then belongs to that
 stream.  There is no fallback: if libsga.so is missing or the device is not an
 sm_100 GPU the calls raise.
 """
@@ -173,9 +174,21 @@ def _strides(shape) -> tuple:
     return tuple(reversed(strides))
 
 
-def _empty(shape, dtype, device):
-    """A contiguous tensor: torch.empty at half its cost, which counts in a decode step's short calls."""
+def _empty(shape, dtype, device, stream=None):
+    """A contiguous tensor: torch.empty at half its cost, which counts in a decode step's short calls.  Its memory belongs
+    to `stream`, the one that the call launches on: on any other, torch could hand it out while that one still uses it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
     return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
+
+
+def _zeros(shape, dtype, device, stream=None):
+    """A tensor of zeros, filled on `stream` (its memory belongs to it, see _empty), or on the current one."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.zeros(shape, dtype=dtype, device=device)
+    return torch.zeros(shape, dtype=dtype, device=device)
 
 
 def _one_device(*tensors):
@@ -203,10 +216,9 @@ def workspace_size(dims: Dims, op: int = OP_FORWARD) -> int:
     return int(out.value)
 
 
-def alloc_workspace(dims: Dims, op: int = OP_FORWARD, device=None) -> torch.Tensor:
-    """A zero-filled workspace (zero = clear device status)."""
-    n = workspace_size(dims, op)
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+def alloc_workspace(dims: Dims, op: int = OP_FORWARD, device=None, stream=None) -> torch.Tensor:
+    """A workspace zero-filled (zero = clear device status) on `stream`, or on the current one."""
+    return _zeros(workspace_size(dims, op), torch.uint8, device or "cuda", stream)
 
 
 def device_status(ws: torch.Tensor, stream=None) -> int:
@@ -229,10 +241,10 @@ def index_scores(q_idx, w, k_idx, q_pos, scores=None, ws=None, stream=None):
     _need(q_pos, "q_pos", torch.int32, (B, T))
     dims = make_dims(B, T, L)
     if scores is None:
-        scores = torch.empty((B, T, L), dtype=torch.float32, device=q_idx.device)
+        scores = _empty((B, T, L), torch.float32, q_idx.device, stream)
     _need(scores, "scores", torch.float32, (B, T, L))
     if ws is None:
-        ws = alloc_workspace(dims, OP_INDEX_SCORES, q_idx.device)
+        ws = alloc_workspace(dims, OP_INDEX_SCORES, q_idx.device, stream=stream)
     _check("sga_index_scores", load_library().sga_index_scores(
         ctypes.byref(dims), _ptr(q_idx), _ptr(w), _ptr(k_idx), _ptr(q_pos), _ptr(scores), _ptr(ws), ws.numel(),
         _stream(stream)))
@@ -249,10 +261,10 @@ def index_scores_fp8(q_idx, w, k_idx, q_pos, scores=None, ws=None, stream=None):
     _need(q_pos, "q_pos", torch.int32, (B, T))
     dims = make_dims(B, T, L)
     if scores is None:
-        scores = torch.empty((B, T, L), dtype=torch.float32, device=q_idx.device)
+        scores = _empty((B, T, L), torch.float32, q_idx.device, stream)
     _need(scores, "scores", torch.float32, (B, T, L))
     if ws is None:
-        ws = alloc_workspace(dims, OP_INDEX_SCORES, q_idx.device)
+        ws = alloc_workspace(dims, OP_INDEX_SCORES, q_idx.device, stream=stream)
     _check("sga_index_scores_fp8", load_library().sga_index_scores_fp8(
         ctypes.byref(dims), _ptr(q_idx), _ptr(w), _ptr(k_idx), _ptr(q_pos), _ptr(scores), _ptr(ws), ws.numel(),
         _stream(stream)))
@@ -266,10 +278,10 @@ def topk_select(scores, q_pos, top_k: int = TOP_K, idx=None, ws=None, stream=Non
     _need(q_pos, "q_pos", torch.int32, (B, T))
     dims = make_dims(B, T, L, top_k)
     if idx is None:
-        idx = torch.empty((B, T, top_k), dtype=torch.int32, device=scores.device)
+        idx = _empty((B, T, top_k), torch.int32, scores.device, stream)
     _need(idx, "idx", torch.int32, (B, T, top_k))
     if ws is None:
-        ws = alloc_workspace(dims, OP_TOPK_SELECT, scores.device)
+        ws = alloc_workspace(dims, OP_TOPK_SELECT, scores.device, stream=stream)
     _check("sga_topk_select", load_library().sga_topk_select(
         ctypes.byref(dims), _ptr(scores), _ptr(q_pos), _ptr(idx), _ptr(ws), ws.numel(), _stream(stream)))
     return idx
@@ -282,7 +294,7 @@ def topk_select_noalloc(scores, q_pos, top_k: int = TOP_K, idx=None, stream=None
     _need(q_pos, "q_pos", torch.int32, (B, T))
     dims = make_dims(B, T, L, top_k)
     if idx is None:
-        idx = torch.empty((B, T, top_k), dtype=torch.int32, device=scores.device)
+        idx = _empty((B, T, top_k), torch.int32, scores.device, stream)
     _need(idx, "idx", torch.int32, (B, T, top_k))
     _check("sga_topk_select_noalloc", load_library().sga_topk_select_noalloc(
         ctypes.byref(dims), _ptr(scores), _ptr(q_pos), _ptr(idx), _stream(stream)))
@@ -301,10 +313,10 @@ def sparse_mla_attend(q, kv, idx, gate=None, out=None, ws=None, stream=None):
         _need(gate, "gate", torch.bfloat16, (B, T, HEADS))
     dims = make_dims(B, T, L, K)
     if out is None:
-        out = torch.empty((B, T, HEADS, V_DIM), dtype=torch.float32, device=q.device)
+        out = _empty((B, T, HEADS, V_DIM), torch.float32, q.device, stream)
     _need(out, "out", torch.float32, (B, T, HEADS, V_DIM))
     if ws is None:
-        ws = alloc_workspace(dims, OP_SPARSE_MLA_ATTEND, q.device)
+        ws = alloc_workspace(dims, OP_SPARSE_MLA_ATTEND, q.device, stream=stream)
     _check("sga_sparse_mla_attend", load_library().sga_sparse_mla_attend(
         ctypes.byref(dims), _ptr(q), _ptr(kv), _ptr(idx), _ptr(gate), _ptr(out), _ptr(ws), ws.numel(),
         _stream(stream)))
@@ -329,14 +341,14 @@ def _forward_call(call: str, fp8: bool, op: int, q_idx, w, k_idx, q, kv, gate, q
     _need(q_pos, "q_pos", torch.int32, (B, T))
     dims = make_dims(B, T, L, top_k)
     if idx_out is None and return_idx:
-        idx_out = torch.empty((B, T, top_k), dtype=torch.int32, device=q.device)
+        idx_out = _empty((B, T, top_k), torch.int32, q.device, stream)
     if idx_out is not None:
         _need(idx_out, "idx_out", torch.int32, (B, T, top_k))
     if out is None:
-        out = torch.empty((B, T, HEADS, V_DIM), dtype=torch.float32, device=q.device)
+        out = _empty((B, T, HEADS, V_DIM), torch.float32, q.device, stream)
     _need(out, "out", torch.float32, (B, T, HEADS, V_DIM))
     if ws is None:
-        ws = alloc_workspace(dims, op, q.device)
+        ws = alloc_workspace(dims, op, q.device, stream=stream)
     _check(call, getattr(load_library(), call)(
         ctypes.byref(dims), _ptr(q_idx), _ptr(w), _ptr(k_idx), _ptr(q), _ptr(kv), _ptr(gate), _ptr(q_pos),
         _ptr(idx_out), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -374,8 +386,8 @@ def forward_fused_fp8(q_idx, w, k_idx, q, kv, gate, q_pos, top_k: int = TOP_K, i
 
 
 # ----------------------------------------------------------------------------- the latent cache in 4 bits
-def _status_ws(device):
-    return torch.zeros(STATUS_BYTES, dtype=torch.uint8, device=device)
+def _status_ws(device, stream):
+    return _zeros(STATUS_BYTES, torch.uint8, device, stream)
 
 
 def kv4_append(kv_rows, q_pos, kv4, ws=None, stream=None):
@@ -387,7 +399,7 @@ def kv4_append(kv_rows, q_pos, kv4, ws=None, stream=None):
     _need(q_pos, "q_pos", torch.int32)
     _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
     if ws is None:
-        ws = _status_ws(kv4.device)
+        ws = _status_ws(kv4.device, stream)
     _one_device(kv_rows, q_pos, kv4, ws)
     st = (_lib or load_library()).sga_kv4_append(
         Dims(B, T, L, TOP_K), kv_rows.data_ptr(), q_pos.data_ptr(), kv4.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -404,11 +416,11 @@ def kv4_read(kv4, pos, kv_rows=None, ws=None, stream=None):
     _need(kv4, "kv4", torch.uint8, (B, L, KV4_ROW_BYTES))
     _need(pos, "pos", torch.int32)
     if kv_rows is None:
-        kv_rows = _empty((B, T, QK_DIM), torch.bfloat16, kv4.device)
+        kv_rows = _empty((B, T, QK_DIM), torch.bfloat16, kv4.device, stream)
     else:
         _need(kv_rows, "kv_rows", torch.bfloat16, (B, T, QK_DIM))
     if ws is None:
-        ws = _status_ws(kv4.device)
+        ws = _status_ws(kv4.device, stream)
     _one_device(kv4, pos, kv_rows, ws)
     st = (_lib or load_library()).sga_kv4_read(
         Dims(B, T, L, TOP_K), kv4.data_ptr(), pos.data_ptr(), kv_rows.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -428,11 +440,11 @@ def sparse_mla_attend_kv4(q, kv4, idx, gate=None, out=None, ws=None, stream=None
     if gate is not None:
         _need(gate, "gate", torch.bfloat16, (B, T, HEADS))
     if out is None:
-        out = _empty((B, T, HEADS, V_DIM), torch.bfloat16, q.device)
+        out = _empty((B, T, HEADS, V_DIM), torch.bfloat16, q.device, stream)
     else:
         _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
     if ws is None:
-        ws = _status_ws(q.device)
+        ws = _status_ws(q.device, stream)
     _one_device(q, kv4, idx, gate, out, ws)
     st = (_lib or load_library()).sga_sparse_mla_attend_kv4(
         Dims(B, T, L, K), q.data_ptr(), kv4.data_ptr(), idx.data_ptr(), _ptr(gate), out.data_ptr(), ws.data_ptr(),
@@ -458,14 +470,14 @@ def forward_kv4(q_idx, w, k_idx, q, kv4, gate, q_pos, top_k: int = TOP_K, idx_ou
     _need(q_pos, "q_pos", torch.int32, (B, T))
     dims = make_dims(B, T, L, top_k)
     if idx_out is None and return_idx:
-        idx_out = torch.empty((B, T, top_k), dtype=torch.int32, device=q.device)
+        idx_out = _empty((B, T, top_k), torch.int32, q.device, stream)
     if idx_out is not None:
         _need(idx_out, "idx_out", torch.int32, (B, T, top_k))
     if out is None:
-        out = _empty((B, T, HEADS, V_DIM), torch.bfloat16, q.device)
+        out = _empty((B, T, HEADS, V_DIM), torch.bfloat16, q.device, stream)
     _need(out, "out", torch.bfloat16, (B, T, HEADS, V_DIM))
     if ws is None:
-        ws = alloc_workspace(dims, OP_FORWARD, q.device)
+        ws = alloc_workspace(dims, OP_FORWARD, q.device, stream=stream)
     _one_device(q_idx, w, k_idx, q, kv4, gate, q_pos, idx_out, out, ws)
     _check("sga_forward_kv4", load_library().sga_forward_kv4(
         ctypes.byref(dims), _ptr(q_idx), _ptr(w), _ptr(k_idx), _ptr(q), _ptr(kv4), _ptr(gate), _ptr(q_pos),
@@ -484,11 +496,12 @@ def quantize_fp8(x, codes=None, scale=None, stream=None):
     K = shape[-1]
     s_shape = (*shape[:-1], -(-K // FP8_BLOCK))
     if codes is None:
-        codes = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        codes = (torch.empty_like(x, dtype=torch.float8_e4m3fn) if stream is None else
+                 _empty(shape, torch.float8_e4m3fn, x.device, stream))
     else:
         _need_fp8(codes, "codes", shape)
     if scale is None:
-        scale = _empty(s_shape, torch.float32, x.device)
+        scale = _empty(s_shape, torch.float32, x.device, stream)
     else:
         _need(scale, "scale", torch.float32, s_shape)
     _one_device(x, codes, scale)
@@ -531,11 +544,11 @@ def gemm_fp8(x, x_scale, w, w_scale, out_dtype=torch.float32, out=None, ws=None,
     if kind is None:
         raise TypeError(f"out_dtype: expected torch.float32 or torch.bfloat16, got {out_dtype}")
     if out is None:
-        out = _empty(y_shape, out_dtype, x.device)
+        out = _empty(y_shape, out_dtype, x.device, stream)
     else:
         _need(out, "out", out_dtype, y_shape)
     if ws is None:
-        ws = _status_ws(x.device)
+        ws = _status_ws(x.device, stream)
     _one_device(x, x_scale, w, w_scale, out, ws)
     st = (_lib or load_library()).sga_gemm_fp8(
         n, M, K, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), kind,
@@ -568,9 +581,10 @@ def layer_workspace_size(dims: Dims, lw: LayerWeights, op: int = LAYER_FORWARD) 
     return int(out.value)
 
 
-def alloc_layer_workspace(dims: Dims, lw: LayerWeights, op: int = LAYER_FORWARD, device=None) -> torch.Tensor:
-    """A zero-filled layer workspace (ready for the first sga_layer_forward)."""
-    return torch.zeros(layer_workspace_size(dims, lw, op), dtype=torch.uint8, device=device or "cuda")
+def alloc_layer_workspace(dims: Dims, lw: LayerWeights, op: int = LAYER_FORWARD, device=None,
+                          stream=None) -> torch.Tensor:
+    """A layer workspace (ready for the first sga_layer_forward), zero-filled on `stream`, or on the current one."""
+    return _zeros(layer_workspace_size(dims, lw, op), torch.uint8, device or "cuda", stream)
 
 
 def _layer_common(wts, h, q_pos, kv_cache, k_idx_cache):
@@ -589,13 +603,13 @@ def layer_project(wts, h, q_pos, kv_cache, k_idx_cache, ws=None, stream=None):
     rows into the caches in place; returns dict(q, gate, q_idx, w), bf16."""
     lw, B, T, L = _layer_common(wts, h, q_pos, kv_cache, k_idx_cache)
     dev = h.device
-    q = torch.empty((B, T, HEADS, QK_DIM), dtype=torch.bfloat16, device=dev)
-    gate = torch.empty((B, T, HEADS), dtype=torch.bfloat16, device=dev)
-    q_idx = torch.empty((B, T, INDEX_HEADS, INDEX_DIM), dtype=torch.bfloat16, device=dev)
-    w = torch.empty((B, T, INDEX_HEADS), dtype=torch.bfloat16, device=dev)
+    q = _empty((B, T, HEADS, QK_DIM), torch.bfloat16, dev, stream)
+    gate = _empty((B, T, HEADS), torch.bfloat16, dev, stream)
+    q_idx = _empty((B, T, INDEX_HEADS, INDEX_DIM), torch.bfloat16, dev, stream)
+    w = _empty((B, T, INDEX_HEADS), torch.bfloat16, dev, stream)
     dims = make_dims(B, T, L)
     if ws is None:
-        ws = alloc_layer_workspace(dims, lw, LAYER_PROJECT, dev)
+        ws = alloc_layer_workspace(dims, lw, LAYER_PROJECT, dev, stream=stream)
     _check("sga_layer_project", load_library().sga_layer_project(
         ctypes.byref(dims), ctypes.byref(lw), _ptr(h), _ptr(q_pos), _ptr(kv_cache), _ptr(k_idx_cache), _ptr(q),
         _ptr(gate), _ptr(q_idx), _ptr(w), _ptr(ws), ws.numel(), _stream(stream)))
@@ -608,11 +622,11 @@ def layer_output(wts, out, y=None, ws=None, stream=None):
     B, T = out.shape[0], out.shape[1]
     _need(out, "out", torch.float32, (B, T, HEADS, V_DIM))
     if y is None:
-        y = torch.empty((B, T, lw.d_model), dtype=torch.float32, device=out.device)
+        y = _empty((B, T, lw.d_model), torch.float32, out.device, stream)
     _need(y, "y", torch.float32, (B, T, lw.d_model))
     dims = make_dims(B, T, 1)
     if ws is None:
-        ws = alloc_layer_workspace(dims, lw, LAYER_OUTPUT, out.device)
+        ws = alloc_layer_workspace(dims, lw, LAYER_OUTPUT, out.device, stream=stream)
     _check("sga_layer_output", load_library().sga_layer_output(
         ctypes.byref(dims), ctypes.byref(lw), _ptr(out), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
     return y
@@ -625,14 +639,14 @@ def layer_forward(wts, h, q_pos, kv_cache, k_idx_cache, top_k: int = TOP_K, idx_
     lw, B, T, L = _layer_common(wts, h, q_pos, kv_cache, k_idx_cache)
     dims = make_dims(B, T, L, top_k)
     if idx_out is None and return_idx:
-        idx_out = torch.empty((B, T, top_k), dtype=torch.int32, device=h.device)
+        idx_out = _empty((B, T, top_k), torch.int32, h.device, stream)
     if idx_out is not None:
         _need(idx_out, "idx_out", torch.int32, (B, T, top_k))
     if y is None:
-        y = torch.empty((B, T, lw.d_model), dtype=torch.float32, device=h.device)
+        y = _empty((B, T, lw.d_model), torch.float32, h.device, stream)
     _need(y, "y", torch.float32, (B, T, lw.d_model))
     if ws is None:
-        ws = alloc_layer_workspace(dims, lw, LAYER_FORWARD, h.device)
+        ws = alloc_layer_workspace(dims, lw, LAYER_FORWARD, h.device, stream=stream)
     _check("sga_layer_forward", load_library().sga_layer_forward(
         ctypes.byref(dims), ctypes.byref(lw), _ptr(h), _ptr(q_pos), _ptr(kv_cache), _ptr(k_idx_cache),
         _ptr(idx_out), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
@@ -660,9 +674,9 @@ def layer_fp8kv4_workspace_size(dims: Dims, lw: LayerFp8Weights) -> int:
     return int(out.value)
 
 
-def alloc_layer_fp8kv4_workspace(dims: Dims, lw: LayerFp8Weights, device=None) -> torch.Tensor:
-    """A zero-filled workspace (ready for the first layer_forward_fp8kv4)."""
-    return torch.zeros(layer_fp8kv4_workspace_size(dims, lw), dtype=torch.uint8, device=device or "cuda")
+def alloc_layer_fp8kv4_workspace(dims: Dims, lw: LayerFp8Weights, device=None, stream=None) -> torch.Tensor:
+    """A workspace (ready for the first layer_forward_fp8kv4), zero-filled on `stream`, or on the current one."""
+    return _zeros(layer_fp8kv4_workspace_size(dims, lw), torch.uint8, device or "cuda", stream)
 
 
 def layer_forward_fp8kv4(wts, h, q_pos, kv4, k_idx_cache, top_k: int = TOP_K, idx_out=None, y=None, ws=None,
@@ -678,14 +692,14 @@ def layer_forward_fp8kv4(wts, h, q_pos, kv4, k_idx_cache, top_k: int = TOP_K, id
     _need(k_idx_cache, "k_idx_cache", torch.bfloat16, (B, L, INDEX_DIM))
     dims = make_dims(B, T, L, top_k)
     if idx_out is None and return_idx:
-        idx_out = torch.empty((B, T, top_k), dtype=torch.int32, device=h.device)
+        idx_out = _empty((B, T, top_k), torch.int32, h.device, stream)
     if idx_out is not None:
         _need(idx_out, "idx_out", torch.int32, (B, T, top_k))
     if y is None:
-        y = torch.empty((B, T, lw.d_model), dtype=torch.float32, device=h.device)
+        y = _empty((B, T, lw.d_model), torch.float32, h.device, stream)
     _need(y, "y", torch.float32, (B, T, lw.d_model))
     if ws is None:
-        ws = alloc_layer_fp8kv4_workspace(dims, lw, h.device)
+        ws = alloc_layer_fp8kv4_workspace(dims, lw, h.device, stream=stream)
     _one_device(h, q_pos, kv4, k_idx_cache, idx_out, y, ws, *wts.values())
     _check("sga_layer_forward_fp8kv4", load_library().sga_layer_forward_fp8kv4(
         ctypes.byref(dims), ctypes.byref(lw), _ptr(h), _ptr(q_pos), _ptr(kv4), _ptr(k_idx_cache), _ptr(idx_out),
@@ -716,14 +730,14 @@ def indexer_warmup(q_idx, w, k_idx, q, kv, idx, grad_k_idx=None, ws=None, stream
     _need(idx, "idx", torch.int32, (B, T, K))
     dev = q_idx.device
     dims = make_dims(B, T, L, K)
-    loss = torch.empty((B, T), dtype=torch.float32, device=dev)
-    grad_q_idx = torch.empty((B, T, INDEX_HEADS, INDEX_DIM), dtype=torch.float32, device=dev)
-    grad_w = torch.empty((B, T, INDEX_HEADS), dtype=torch.float32, device=dev)
+    loss = _empty((B, T), torch.float32, dev, stream)
+    grad_q_idx = _empty((B, T, INDEX_HEADS, INDEX_DIM), torch.float32, dev, stream)
+    grad_w = _empty((B, T, INDEX_HEADS), torch.float32, dev, stream)
     if grad_k_idx is None:
-        grad_k_idx = torch.zeros((B, L, INDEX_DIM), dtype=torch.float32, device=dev)
+        grad_k_idx = _zeros((B, L, INDEX_DIM), torch.float32, dev, stream)
     _need(grad_k_idx, "grad_k_idx", torch.float32, (B, L, INDEX_DIM))
     if ws is None:
-        ws = torch.zeros(indexer_warmup_workspace_size(dims), dtype=torch.uint8, device=dev)
+        ws = _zeros(indexer_warmup_workspace_size(dims), torch.uint8, dev, stream)
     _check("sga_indexer_warmup", load_library().sga_indexer_warmup(
         ctypes.byref(dims), _ptr(q_idx), _ptr(w), _ptr(k_idx), _ptr(q), _ptr(kv), _ptr(idx), _ptr(loss),
         _ptr(grad_q_idx), _ptr(grad_w), _ptr(grad_k_idx), _ptr(ws), ws.numel(), _stream(stream)))
