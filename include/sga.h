@@ -290,7 +290,9 @@ typedef enum { SGA_OUT_FP32 = 0, SGA_OUT_BF16 = 1 } sga_out_type_t;
  *   x [n][k] E4M3 bytes    x_scale [n][ceil(k / 128)] fp32
  *   w [m][k] E4M3 bytes    w_scale [ceil(m / 128)][ceil(k / 128)] fp32
  *   y [n][m] fp32 or bf16 (out_type)
- * The scales are any fp32 values.  A block's products accumulate in fp32 in
+ * The scales are any fp32 values.  (Where the product of two leaves fp32's
+ * normal range, the elements concerned are computed once more without tensor
+ * cores, which takes far longer.)  A block's products accumulate in fp32 in
  * the tensor core, the scaled blocks in fp32 in a fixed order (results do not
  * depend on the schedule); a bf16 y is rounded once.  k is a multiple of 16; x
  * and w 16-byte aligned, y aligned to its elements.  The last blocks may be

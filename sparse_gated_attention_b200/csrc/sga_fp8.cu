@@ -22,8 +22,10 @@
 // 256 columns, and by power at large sizes: 4096 x 7168 x 8192 227 us on zeros, 264 on data, 1.8 PFLOP/s (the MMAs alone
 // 147).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -38,6 +40,80 @@ namespace {
 
 constexpr int kBlock = 128;  // K elements (bytes) and weight rows that share a scale
 constexpr int kMaxExtent = 1 << 30;  // of any dimension: the last tile's end stays within an int
+
+// ---------------------------------------------------------------- pairs of scales past fp32's range
+// Both kernels multiply a block's sum v by x_scale * w_scale.  Where that product is no normal fp32 number (it
+// overflows, or loses bits as a subnormal or zero) v * x_scale * w_scale may still be one: v is zero or between 2^-18
+// and 2^25 in magnitude (E4M3 products are multiples of 2^-18).  Such pairs are rare, and a branch in the accumulating
+// loops costs 3% to 20% of the large products.  So the warps that fetch the scales only note that the thread block met
+// one, and after its last tile it looks for the elements concerned and computes them once more, here.
+
+// Zero, subnormal, infinite or NaN.
+__device__ __forceinline__ bool not_normal(float s) {
+  return (__float_as_uint(s) & 0x7FFFFFFFu) - 0x00800000u >= 0x7F000000u;
+}
+
+// The largest and the least magnitude but zero of the scales seen so far, as their bits (a NaN is the largest).
+struct ScaleRange {
+  uint32_t big = 0, small_1 = 0xFFFFFFFFu;  // the least, minus one: a zero is the largest there
+  __device__ __forceinline__ void see(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+    big = max(big, b);
+    small_1 = min(small_1, b - 1u);
+  }
+  // Whether one of them may have no normal product with w (those of zeros are zero, as they should be).
+  __device__ __forceinline__ bool odd_with(float w) const {
+    return w != 0.f && big != 0 &&
+           (not_normal(__uint_as_float(big) * w) || not_normal(__uint_as_float(small_1 + 1u) * w));
+  }
+};
+
+// The product as s * pre: pre is a power of two, v * pre is exact, and v * pre * s rounds once.
+struct ScalePair {
+  float s, pre;
+};
+__device__ __forceinline__ ScalePair scale_pair(float x, float w) {
+  const float s = x * w;
+  const float big = fmaxf(fabsf(x), fabsf(w)), small = fminf(fabsf(x), fabsf(w));
+  // zeros and infinities are what they are; so is NaN (which fmaxf and fminf leave out)
+  if (!not_normal(s) || isnan(s) || small == 0.f || isinf(big)) return {s, 1.f};
+  if (fabsf(s) <= 1.f) return {copysignf(small * 0x1p100f * big, s), 0x1p-100f};
+  // a rest of 2^128 and more times v is infinite for every v but zero, and so is FLT_MAX
+  return {copysignf(fminf(big * 0x1p-100f * small, FLT_MAX), s), 0x1p100f};
+}
+
+__device__ __noinline__ bool any_odd_pair(const float* xs, const float* ws, int k_blocks) {
+  bool odd = false;
+#pragma unroll 1
+  for (int kb = 0; kb < k_blocks; ++kb) odd |= scale_pair(xs[kb], ws[kb]).pre != 1.f;
+  return odd;
+}
+
+// One output element, from its rows and their scales.
+__device__ __noinline__ float scaled_dot(const uint8_t* x, const uint8_t* w, const float* xs, const float* ws, int k) {
+  float acc = 0.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < k; c0 += kBlock) {
+    float v = 0.f;
+#pragma unroll 1
+    for (int c = c0; c < min(c0 + kBlock, k); c += 16) {  // k is a multiple of 16
+      const uint4 a = *reinterpret_cast<const uint4*>(x + c), b = *reinterpret_cast<const uint4*>(w + c);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const auto pair = [&](const uint32_t (&q)[4]) {
+          const auto two = static_cast<__nv_fp8x2_storage_t>(q[i >> 1] >> (16 * (i & 1)));
+          return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+        };
+        const float2 fa = pair(aw), fb = pair(bw);
+        v = fmaf(fa.y, fb.y, fmaf(fa.x, fb.x, v));
+      }
+    }
+    const ScalePair sp = scale_pair(xs[c0 / kBlock], ws[c0 / kBlock]);
+    acc = fmaf(v * sp.pre, sp.s, acc);
+  }
+  return acc;
+}
 
 // ---------------------------------------------------------------- quantiser
 constexpr int kQuantLanes = 16;  // threads per block of 128: 8 values (16 bytes) each
@@ -142,8 +218,10 @@ struct StreamCfg {
 };
 
 struct StreamParams {
-  int n, m, n_blocks, tiles, k_blocks, units;  // tiles: 128 weight rows x NP tokens; units: pairs of K blocks in one
-  int splits;                                  // thread blocks (a cluster) that share a tile's K
+  int n, m, k, n_blocks, tiles, k_blocks, units;  // tiles: 128 weight rows x NP tokens; units: pairs of K blocks in one
+  int splits;                                     // thread blocks (a cluster) that share a tile's K
+  const uint8_t* x;
+  const uint8_t* w;
   const float* x_scale;
   const float* w_scale;
   float* out_f32;
@@ -170,6 +248,29 @@ __device__ __forceinline__ void store_y(const StreamParams& p, int row, int toke
   }
 }
 
+// Computes this thread's outputs of every tile of its thread block once more where a block's scales have no normal
+// product.  (By itself, so that nothing of it is held in registers meanwhile.)
+template <int NP>
+__device__ __noinline__ void redo_stream_tiles(StreamParams p) {
+  using Cfg = StreamCfg<NP>;
+  const int warp = threadIdx.x >> 5, mrow = (warp & 3) * 32 + (threadIdx.x & 31), group = (warp - 4) >> 2;
+  const int rank = blockIdx.x % p.splits;
+  // the same thread wrote them
+  const int c0 = p.splits == 1 ? group * Cfg::kCols : NP * rank / p.splits + group;
+  const int c1 = p.splits == 1 ? c0 + Cfg::kCols : NP * (rank + 1) / p.splits;
+  for (int t = blockIdx.x / p.splits; t < p.tiles; t += gridDim.x / p.splits) {
+    const int row = t / p.n_blocks * kTileM + mrow, token0 = t % p.n_blocks * NP;
+    if (row >= p.m) continue;
+    const float* ws = p.w_scale + static_cast<size_t>(row / kBlock) * p.k_blocks;
+    for (int i = token0 + c0; i < min(token0 + c1, p.n); i += p.splits == 1 ? 1 : Cfg::kGroups) {
+      const float* xs = p.x_scale + static_cast<size_t>(i) * p.k_blocks;
+      if (!any_odd_pair(xs, ws, p.k_blocks)) continue;
+      const float y = scaled_dot(p.x + static_cast<size_t>(i) * p.k, p.w + static_cast<size_t>(row) * p.k, xs, ws, p.k);
+      store_y<1>(p, row, i, 0, 1, [&](int) { return y; });
+    }
+  }
+}
+
 template <int NP>
 __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     gemm_fp8_stream_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -191,6 +292,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
   const uint32_t done_bar = bar0 + 8u * (2 * Cfg::kStages + 2 * kAccBufs + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* odd_scales = reinterpret_cast<volatile int*>(tmem_slot + 2);  // such a pair was met
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
   // This thread block's tiles (token blocks fastest, so that neighbours share weights) and its part [u0, u1) of each
@@ -215,6 +317,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
+    *odd_scales = 0;
     fence_barrier_init();
     prefetch_tmap(&wmap);
     prefetch_tmap(&xmap);
@@ -351,7 +454,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     const int t64 = threadIdx.x - 64;
     int slot = 0;
     uint32_t ph = 0;
-    bool ok = true;
+    bool ok = true, odd = false;
     for (int t = first; t < p.tiles && ok; t += step) {
       const float* ws = p.w_scale + static_cast<size_t>(t / p.n_blocks) * p.k_blocks;
       const int token0 = t % p.n_blocks * NP;
@@ -372,6 +475,10 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NP / 4; ++i) dst[kbl * NP + tok0 + 4 * i] = v[i] * wv;
         mbar_arrive(sfull(slot));
+        ScaleRange range;
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i) range.see(v[i]);
+        odd |= range.odd_with(wv);
         slot ^= 1;
         if (slot == 0) ph ^= 1u;
       }
@@ -380,6 +487,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
     }
+    if (odd) *odd_scales = 1;
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scaled accumulation
@@ -494,6 +602,9 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
   }
   if (warp < 4 && p.splits > 1) {
     cluster_barrier();
+    // the thread blocks that write the tile's output have to know
+    if ((warp == 2 || warp == 3) && lane < p.splits && *odd_scales)
+      st_cluster(map_to_rank(smem_u32(tmem_slot + 2), lane), __uint_as_float(1u));
     cluster_barrier();
   }
 
@@ -503,6 +614,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (*odd_scales && !*abort_flag && warp >= 4) redo_stream_tiles<NP>(p);
 }
 
 // What the kernel takes for `tiles` tiles of NP tokens, in microseconds, and the split of K it takes it with.  Fitted to
@@ -535,6 +647,9 @@ cudaError_t launch_stream(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   StreamParams p;
   p.n = a.n;
   p.m = a.m;
+  p.k = a.k;
+  p.x = a.x;
+  p.w = a.w;
   p.n_blocks = (a.n + NP - 1) / NP;
   const long long tiles = static_cast<long long>((a.m + kTileM - 1) / kTileM) * p.n_blocks;
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
@@ -589,12 +704,15 @@ constexpr int kTOutFloats = 32 * 33;           // one accumulating warp's 32 x 3
 constexpr size_t kTSmem =
     1024 + kTStages * kTStageBytes + (2 * kTScaleFloats + 8 * kTOutFloats) * 4 + kTNumBars * 8 + 16;
 static_assert(kTSmem <= 232448, "shared memory budget");
-// Registers at launch: 384 threads x 168 = 64,512, shared out as 128 x 56 + 256 x 224.
-constexpr int kTRegsSmall = 56, kTRegsLarge = 224;
+// Registers at launch: 384 threads x 168 = 64,512, shared out as 128 x 64 + 256 x 216.  (With 56 and 224 the compiler
+// spills 100 bytes where the scales' range is kept, and a large product takes 8% longer.)
+constexpr int kTRegsSmall = 64, kTRegsLarge = 216;
 static_assert(128 * kTRegsSmall + 256 * kTRegsLarge <= 384 * 168, "register split");
 
 struct TileParams {
-  int n, m, n_tiles, m_tiles, k_blocks, tiles;
+  int n, m, k, n_tiles, m_tiles, k_blocks, tiles;
+  const uint8_t* x;
+  const uint8_t* w;
   const float* x_scale;
   const float* w_scale;
   float* out_f32;
@@ -613,6 +731,28 @@ __device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float
       "mov.b64 {%0, %1}, c;\n\t}"
       : "+f"(a), "+f"(b)
       : "f"(x), "f"(y), "f"(s));
+}
+
+// As redo_stream_tiles: a thread takes a token's channels of one block of weight rows.
+__device__ __noinline__ void redo_tiles(TileParams p) {
+  const int warp = threadIdx.x >> 5, tok = (warp & 3) * 32 + (threadIdx.x & 31), half = (warp - 4) >> 2;
+  for (int t = blockIdx.x >> 1; t < p.tiles; t += gridDim.x >> 1) {
+    const int token = (2 * (t % p.n_tiles) + (blockIdx.x & 1)) * kTM + tok, ch0 = t / p.n_tiles * kTN + half * kBlock;
+    if (token >= p.n || ch0 >= p.m) continue;
+    const float* xs = p.x_scale + static_cast<size_t>(token) * p.k_blocks;
+    const float* ws = p.w_scale + static_cast<size_t>(ch0 / kBlock) * p.k_blocks;
+    if (!any_odd_pair(xs, ws, p.k_blocks)) continue;
+    const uint8_t* x = p.x + static_cast<size_t>(token) * p.k;
+    for (int ch = ch0; ch < min(ch0 + kBlock, p.m); ++ch) {
+      const float y = scaled_dot(x, p.w + static_cast<size_t>(ch) * p.k, xs, ws, p.k);
+      const size_t at = static_cast<size_t>(token) * p.m + ch;
+      if (p.out_bf16) {
+        p.out_bf16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+      } else {
+        p.out_f32[at] = y;
+      }
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kTThreads, 1)
@@ -634,6 +774,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   auto done = [&](int a) { return bar0 + 8u * (2 * kTStages + 8 + a); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kTNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* odd_scales = reinterpret_cast<volatile int*>(tmem_slot + 2);  // such a pair was met
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
 
@@ -650,6 +791,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(done(a), 1);
     }
     *abort_flag = 0;
+    *odd_scales = 0;
     fence_barrier_init();
     prefetch_tmap(&wmap);
     prefetch_tmap(&xmap);
@@ -781,6 +923,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
           // 16 loads before their stores (addresses past the end are clamped, their values dropped)
           const int kbl = lane % kTChunk, tok0 = lane / kTChunk, kb = kb0 + kbl;
           const float* col = p.x_scale + min(kb, p.k_blocks - 1);
+          // the lane's K block of the channel blocks 2 tm and 2 tm + 1
+          const float* wrow = p.w_scale + static_cast<size_t>(2 * tm) * p.k_blocks + min(kb, p.k_blocks - 1);
+          const float w0 = __ldg(wrow), w1 = 2 * tm + 1 < m_blocks ? __ldg(wrow + p.k_blocks) : 0.f;
+          ScaleRange range;
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {
             const int tok1 = tok0 + part * (kTM / 2);
@@ -790,13 +936,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
               v[i] = __ldg(col + static_cast<size_t>(min((2 * tn + rank) * kTM + tok1 + 4 * i, p.n - 1)) * p.k_blocks);
 #pragma unroll
             for (int i = 0; i < 16; ++i) dst[kbl * kTScaleLd + tok1 + 4 * i] = v[i];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) range.see(v[i]);
           }
-          if (lane < 2 * kTChunk) {
-            const int mb = 2 * tm + lane / kTChunk;
-            dst[kTChunk * kTScaleLd + lane] = kb < p.k_blocks && mb < m_blocks
-                                                  ? __ldg(p.w_scale + static_cast<size_t>(mb) * p.k_blocks + kb)
-                                                  : 0.f;
+          if (lane < kTChunk) {
+            dst[kTChunk * kTScaleLd + lane] = w0;
+            dst[kTChunk * kTScaleLd + kTChunk + lane] = w1;
           }
+          if (range.odd_with(w0) || range.odd_with(w1)) *odd_scales = 1;
           mbar_arrive(sfull(slot));
           slot ^= 1;
           if (slot == 0) ph ^= 1u;
@@ -895,6 +1042,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       record_status(p.status, kStatusTimeout);
       *abort_flag = 1;
     }
+    if (ok && *odd_scales) redo_tiles(p);
   }
 
   tc_fence_before();
@@ -910,6 +1058,9 @@ cudaError_t launch_tile(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
   TileParams p;
   p.n = a.n;
   p.m = a.m;
+  p.k = a.k;
+  p.x = a.x;
+  p.w = a.w;
   p.n_tiles = (a.n + 2 * kTM - 1) / (2 * kTM);
   p.m_tiles = (a.m + kTN - 1) / kTN;
   p.k_blocks = (a.k + kBlock - 1) / kBlock;

@@ -201,6 +201,54 @@ def test_product_propagates_nan_and_infinite_scales_to_their_rows_only():
     assert not bool((bad & keep).any())
 
 
+# pairs of scales whose product fp32 cannot hold (or only as a subnormal, with fewer bits), or just can
+EXTREME_SCALES = [(2.0 ** -100, 2.0 ** -60), (1.7 * 2.0 ** -126, 1.3 * 2.0 ** -20), (2.0 ** -149, 1.9 * 2.0 ** 3),
+                  (1.5 * 2.0 ** 100, 1.1 * 2.0 ** 40), (2.0 ** 120, 2.0 ** 8), (1.9 * 2.0 ** 127, 1.9 * 2.0 ** 18),
+                  (1.3 * 2.0 ** 90, 2.0 ** -140), (2.0 ** -70, 1.7 * 2.0 ** -56), (1.2 * 2.0 ** 64, 1.6 * 2.0 ** 63),
+                  (0.0, 2.0 ** 127), (2.0 ** -149, 2.0 ** -149), (2.0 ** 127, 2.0 ** 127)]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,m,k", [(7, 260, 400), (30, 260, 4000), (60, 260, 1680), (100, 260, 2064), (1100, 2050, 528)])
+def test_product_scales_over_the_whole_range(n, m, k, out_dtype):
+    """Scales as far as fp32 goes.  A token has codes in one K block, where its scale meets the block's partner (or the
+    next pair's), and zeros in the others, where it meets any.  Codes are powers of two of every size, so nothing
+    cancels.  Near the bottom every product and sum may also be off by a step of 2^-149 (2^-133 of a bf16 result);
+    results past the largest value are infinite, and sums of zeros stay zero whatever their scales."""
+    g = gen(n + k)
+    kb, mb = -(-k // 128), -(-m // 128)
+    x = torch.zeros((n, k), device=DEV)
+    xs = torch.ones((n, kb), device=DEV)
+    ws = torch.empty((mb, kb), device=DEV)
+    for j in range(kb):
+        ws[:, j] = EXTREME_SCALES[j % len(EXTREME_SCALES)][1]
+    power = lambda *shape: torch.exp2(torch.randint(-9, 9, shape, generator=g, device=DEV).float())
+    for t in range(n):
+        j = t % kb
+        xs[t] = EXTREME_SCALES[(j + (t % 3 == 0)) % len(EXTREME_SCALES)][0]
+        width = min(128, k - 128 * j)
+        if t % 5:  # else a token of zeros
+            x[t, 128 * j:128 * j + width] = power(width) * (1 if t % 2 else 2.0 ** -9)
+    w = power(m, k) * torch.where(torch.rand((m, 1), generator=g, device=DEV) < 0.1, 0.0, 1.0)
+    x8, w8 = x.clamp(max=256).to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+    y = sga.gemm_fp8(x8, xs, w8, ws, out_dtype=out_dtype)
+    X = x8.double() * xs.double().repeat_interleave(128, 1)[:, :k]
+    W = w8.double() * ws.double().repeat_interleave(128, 0)[:m].repeat_interleave(128, 1)[:, :k]
+    want = X @ W.T  # fp64 holds every product: of positive numbers, nothing cancels
+    top = torch.finfo(out_dtype).max
+    half = 2.0 ** -8 if out_dtype == torch.bfloat16 else 0.0
+    tiny = 2.0 ** -133 if out_dtype == torch.bfloat16 else 2.0 ** -149
+    tol = (k + 2 * kb + 2) * 2.0 ** -23 * want + half * want + tiny + (kb + 1) * 2.0 ** -149
+    got = y.double()
+    big = want > top * (1 + 2.0 ** -6)
+    near = (want > top * (1 - 2.0 ** -6)) & ~big  # may round either way
+    assert torch.equal(torch.isinf(got) | near, big | near)
+    finite = ~big & ~near
+    assert bool(((got - want).abs() <= tol)[finite].all())
+    assert not bool(got[want == 0].any())
+    assert int(big.sum()) > 0 and int((finite & (want > 0)).sum()) > 0
+
+
 def test_product_leading_dims_and_out():
     x, xs, w, wsc = product_case(6, 96, 256, 5)
     want = sga.gemm_fp8(x, xs, w, wsc, out_dtype=torch.bfloat16)
