@@ -206,8 +206,22 @@ def _need_fp8(t, name, shape=None):
     return _need(t, name, torch.uint8, shape)
 
 
+def _too_long(*extents):
+    raise ValueError(f"extents of at most 2^31 - 1 expected, got {extents}")
+
+
 def make_dims(batch: int, n_q: int, kv_stride: int, top_k: int = TOP_K) -> Dims:
-    return Dims(int(batch), int(n_q), int(kv_stride), int(top_k))
+    extents = (int(batch), int(n_q), int(kv_stride), int(top_k))
+    if max(extents) >> 31 or min(extents) >> 31 < -1:  # ctypes would keep the low 32 bits
+        _too_long(*extents)
+    return Dims(*extents)
+
+
+def _shape_dims(B, T, L, K):
+    """make_dims of extents that come from tensors' shapes."""
+    if (B | T | L | K) >> 31:
+        _too_long(B, T, L, K)
+    return Dims(B, T, L, K)
 
 
 def workspace_size(dims: Dims, op: int = OP_FORWARD) -> int:
@@ -402,7 +416,7 @@ def kv4_append(kv_rows, q_pos, kv4, ws=None, stream=None):
         ws = _status_ws(kv4.device, stream)
     _one_device(kv_rows, q_pos, kv4, ws)
     st = (_lib or load_library()).sga_kv4_append(
-        Dims(B, T, L, TOP_K), kv_rows.data_ptr(), q_pos.data_ptr(), kv4.data_ptr(), ws.data_ptr(), ws.numel(),
+        _shape_dims(B, T, L, TOP_K), kv_rows.data_ptr(), q_pos.data_ptr(), kv4.data_ptr(), ws.data_ptr(), ws.numel(),
         _stream(stream))
     if st:
         raise SGAError("sga_kv4_append", st)
@@ -423,7 +437,7 @@ def kv4_read(kv4, pos, kv_rows=None, ws=None, stream=None):
         ws = _status_ws(kv4.device, stream)
     _one_device(kv4, pos, kv_rows, ws)
     st = (_lib or load_library()).sga_kv4_read(
-        Dims(B, T, L, TOP_K), kv4.data_ptr(), pos.data_ptr(), kv_rows.data_ptr(), ws.data_ptr(), ws.numel(),
+        _shape_dims(B, T, L, TOP_K), kv4.data_ptr(), pos.data_ptr(), kv_rows.data_ptr(), ws.data_ptr(), ws.numel(),
         _stream(stream))
     if st:
         raise SGAError("sga_kv4_read", st)
@@ -447,7 +461,7 @@ def sparse_mla_attend_kv4(q, kv4, idx, gate=None, out=None, ws=None, stream=None
         ws = _status_ws(q.device, stream)
     _one_device(q, kv4, idx, gate, out, ws)
     st = (_lib or load_library()).sga_sparse_mla_attend_kv4(
-        Dims(B, T, L, K), q.data_ptr(), kv4.data_ptr(), idx.data_ptr(), _ptr(gate), out.data_ptr(), ws.data_ptr(),
+        _shape_dims(B, T, L, K), q.data_ptr(), kv4.data_ptr(), idx.data_ptr(), _ptr(gate), out.data_ptr(), ws.data_ptr(),
         ws.numel(), _stream(stream))
     if st:
         raise SGAError("sga_sparse_mla_attend_kv4", st)
@@ -494,6 +508,8 @@ def quantize_fp8(x, codes=None, scale=None, stream=None):
     if n == 0 or not shape:
         raise ValueError("x: must be [..., K] with at least one element")
     K = shape[-1]
+    if (K | n // K) >> 31:
+        _too_long(n // K, K)
     s_shape = (*shape[:-1], -(-K // FP8_BLOCK))
     if codes is None:
         codes = (torch.empty_like(x, dtype=torch.float8_e4m3fn) if stream is None else
@@ -524,6 +540,8 @@ def _gemm_fp8_shapes(x_shape, w_shape):
         n *= d
     if n == 0 or M == 0 or K == 0:
         raise ValueError("x, w: must have at least one element")
+    if (n | M | K) >> 31:
+        _too_long(n, M, K)
     kb = -(-K // FP8_BLOCK)
     return n, (*lead, kb), (-(-M // FP8_BLOCK), kb), (*lead, M)
 

@@ -161,6 +161,42 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
                                   torch.zeros((1, 1, 64), dtype=i32))
 
 
+def test_binding_refuses_extents_past_32_bits(monkeypatch):
+    """The library takes 32-bit extents: a longer one is refused, not cut to its low bits (the first tensor here would
+    be quantised in its first 16 channels only)."""
+    from sparse_gated_attention_b200 import _binding
+
+    def big(*shape, dtype=torch.uint8):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    monkeypatch.setattr(_binding, "_need", lambda t, *a: t)
+    monkeypatch.setattr(_binding, "_one_device", lambda *t: None)
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    with pytest.raises(ValueError, match="2\\^31"):
+        sga.quantize_fp8(big(1, 2 ** 32 + 16, dtype=bf))
+    with pytest.raises(ValueError, match="2\\^31"):
+        sga.quantize_fp8(big(2 ** 32 + 1, 16, dtype=bf))
+    for x, w in ((big(1, 16), big(2 ** 32 + 5, 16)), (big(1, 2 ** 32 + 16), big(3, 2 ** 32 + 16)),
+                 (big(2 ** 31, 2, 16), big(3, 16))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            sga.gemm_fp8(x, big(1, dtype=f32), w, big(1, dtype=f32))
+    row, q, cache = big(1, 1, 576, dtype=bf), big(1, 1, 64, 576, dtype=bf), big(1, 2 ** 32 + 8, 416)
+    pos, ws = big(1, 1, dtype=i32), big(256)
+    with pytest.raises(ValueError, match="2\\^31"):
+        sga.kv4_append(row, pos, cache, ws=ws)
+    with pytest.raises(ValueError, match="2\\^31"):
+        sga.kv4_read(cache, pos, row, ws=ws)
+    with pytest.raises(ValueError, match="2\\^31"):
+        sga.sparse_mla_attend_kv4(q, cache, big(1, 1, 64, dtype=i32), out=q, ws=ws)
+    with pytest.raises(ValueError, match="2\\^31"):
+        sga.sparse_mla_attend_kv4(q, big(1, 8, 416), big(1, 1, 2 ** 32 + 64, dtype=i32), out=q, ws=ws)
+    for extents in ((2 ** 32 + 1, 1, 1), (1, 2 ** 31, 1), (1, 1, 2 ** 32 + 5), (1, 1, 5, 2 ** 32 + 64),
+                    (5 - 2 ** 32, 1, 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            sga.make_dims(*extents)
+    assert sga.make_dims(1, 2, 3, 2 ** 31 - 1).top_k == 2 ** 31 - 1
+
+
 def _fp8_weights(d_model=7168, q_rank=1536, **bad):
     names = ("w_hq", "w_hq_scale", "w_cq", "w_cq_scale", "w_o", "w_o_scale", "w_uk", "w_uv")
     return sga.LayerFp8Weights(d_model, q_rank, *(bad.get(n, 0x300000 + 0x100000 * i) for i, n in enumerate(names)))
