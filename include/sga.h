@@ -461,7 +461,7 @@ SGA_API sga_status_t sga_layer_forward(const sga_dims_t* dims, const sga_layer_w
  *        (8,192) from 12,416
  *   w_o  [D][8192]
  *   w_uk, w_uv [64][128][512] bf16, as for sga_layer_forward
- * D = d_model and R = q_rank are multiples of 16.                             */
+ * D = d_model and R = q_rank are multiples of 16, at most 2^30.               */
 typedef struct {
   int32_t d_model; /* D */
   int32_t q_rank;  /* R */

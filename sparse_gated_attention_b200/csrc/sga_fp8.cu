@@ -39,7 +39,6 @@ namespace sga {
 namespace {
 
 constexpr int kBlock = 128;  // K elements (bytes) and weight rows that share a scale
-constexpr int kMaxExtent = 1 << 30;  // of any dimension: the last tile's end stays within an int
 
 // ---------------------------------------------------------------- pairs of scales past fp32's range
 // Both kernels multiply a block's sum v by x_scale * w_scale.  Where that product is no normal fp32 number (it

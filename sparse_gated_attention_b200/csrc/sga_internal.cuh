@@ -107,6 +107,7 @@ cudaError_t launch_kv4_append(const uint16_t* kv_rows, const int32_t* q_pos, uin
                               int n_q, int kv_stride, cudaStream_t s);
 
 // ---- E4M3 products with a scale per block of 128 ----------------------------------------
+constexpr int kMaxExtent = 1 << 30;  // of any of their dimensions: the last tile's end stays within an int
 cudaError_t launch_quantize_fp8(int rows, int cols, const uint16_t* x, uint8_t* codes, float* scale, cudaStream_t s);
 struct GemmFp8Args {
   int n, m, k;

@@ -486,6 +486,7 @@ bool layer_dims_ok8(const sga_dims_t* d, const sga_layer_fp8_weights_t* W) {
   if (d->batch < 1 || d->n_q < 1 || d->kv_stride < 1 || d->kv_stride > SGA_MAX_KV_STRIDE) return false;
   if (d->top_k < 64 || d->top_k > SGA_MAX_TOP_K || d->top_k % 64 != 0) return false;
   if (W->d_model < 16 || W->d_model % 16 != 0 || W->q_rank < 16 || W->q_rank % 16 != 0) return false;
+  if (W->d_model > sga::kMaxExtent || W->q_rank > sga::kMaxExtent) return false;
   const long long rows = static_cast<long long>(d->batch) * d->n_q;
   if (rows * kHeads * kLatent > INT32_MAX || rows * (W->q_rank + kBlock8 + kHqExtra8) > INT32_MAX) return false;
   return static_cast<long long>(d->batch) * d->kv_stride <= INT32_MAX;

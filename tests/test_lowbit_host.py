@@ -223,3 +223,18 @@ def test_layer_fp8kv4_workspace_and_refusals(lib):
     out = ctypes.c_size_t(0)
     assert lib.sga_layer_fp8kv4_workspace_size(r, None, ctypes.byref(out)) == 1
     assert lib.sga_layer_fp8kv4_workspace_size(r, ctypes.byref(_fp8_weights()), None) == 1
+
+
+def test_layer_sizes_past_2_to_30_are_refused(lib):
+    """A width near 2^31 made the size checks wrap, and gave a workspace size that had wrapped as well."""
+    out = ctypes.c_size_t(0)
+    d = ctypes.byref(sga.make_dims(1, 1, 100))
+    top = 1 << 30
+    for width in (top + 16, 2 ** 31 - 1024, 2 ** 31 - 16):
+        for bad in (dict(d_model=width), dict(q_rank=width)):
+            W = _fp8_weights(**bad)
+            assert lib.sga_layer_fp8kv4_workspace_size(d, ctypes.byref(W), ctypes.byref(out)) == 1, bad
+            assert lib.sga_layer_forward_fp8kv4(d, ctypes.byref(W), GOOD, GOOD, GOOD, GOOD, None, GOOD, WS, 1 << 60,
+                                                None) == 1, bad
+    assert lib.sga_layer_fp8kv4_workspace_size(d, ctypes.byref(_fp8_weights(q_rank=top)), ctypes.byref(out)) == 0
+    assert out.value > top * 7  # codes, g1 and c_q of one token
