@@ -388,9 +388,9 @@ SGA_API sga_status_t sga_topk_select_noalloc(const sga_dims_t* dims, const float
  *   w_uk [64][128][512]:      k_nope_h = w_uk[h] c_kv
  *   w_uv [64][128][512]:      o_h = w_uv[h] out_h
  *   w_o  [D][8192]
- * D = d_model (7168 in A.X K2) and R = q_rank (1536) are multiples of 8; every
- * weight pointer is 16-byte aligned.  The new tokens of one sequence must
- * have distinct positions.                                                   */
+ * D = d_model (7168 in A.X K2) and R = q_rank (1536) are multiples of 8, at
+ * most 2^30; every weight pointer is 16-byte aligned.  The new tokens of one
+ * sequence must have distinct positions.                                     */
 
 typedef struct {
   int32_t d_model; /* D */
@@ -461,7 +461,8 @@ SGA_API sga_status_t sga_layer_forward(const sga_dims_t* dims, const sga_layer_w
  *        (8,192) from 12,416
  *   w_o  [D][8192]
  *   w_uk, w_uv [64][128][512] bf16, as for sga_layer_forward
- * D = d_model and R = q_rank are multiples of 16, at most 2^30.               */
+ * D = d_model and R = q_rank are multiples of 16, at most 2^30.  The new tokens
+ * of one sequence must have distinct positions.                              */
 typedef struct {
   int32_t d_model; /* D */
   int32_t q_rank;  /* R */

@@ -90,6 +90,8 @@ struct AttendArgs {
 int attend_splits(int rows, int top_k);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream);
 
+constexpr int kMaxExtent = 1 << 30;  // of a projection's dimensions: the last tile's end stays within an int
+
 // ---- attention over the 4-bit latent cache ------------------------------------------
 struct Attend4Args {
   const uint16_t* q;     // [rows][64][576]
@@ -107,7 +109,6 @@ cudaError_t launch_kv4_append(const uint16_t* kv_rows, const int32_t* q_pos, uin
                               int n_q, int kv_stride, cudaStream_t s);
 
 // ---- E4M3 products with a scale per block of 128 ----------------------------------------
-constexpr int kMaxExtent = 1 << 30;  // of any of their dimensions: the last tile's end stays within an int
 cudaError_t launch_quantize_fp8(int rows, int cols, const uint16_t* x, uint8_t* codes, float* scale, cudaStream_t s);
 struct GemmFp8Args {
   int n, m, k;

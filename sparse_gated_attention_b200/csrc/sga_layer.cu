@@ -322,6 +322,7 @@ bool layer_dims_ok(const sga_dims_t* d, const sga_layer_weights_t* W) {
   if (!d || !W) return false;
   if (d->batch < 1 || d->n_q < 1 || d->kv_stride < 1 || d->kv_stride > SGA_MAX_KV_STRIDE) return false;
   if (W->d_model < 8 || W->d_model % 8 != 0 || W->q_rank < 8 || W->q_rank % 8 != 0) return false;
+  if (W->d_model > sga::kMaxExtent || W->q_rank > sga::kMaxExtent) return false;
   const long long rows = static_cast<long long>(d->batch) * d->n_q;
   if (rows * kCqRows > INT32_MAX || rows * kHeads * kLatent > INT32_MAX) return false;
   if (static_cast<long long>(d->batch) * d->kv_stride > INT32_MAX) return false;

@@ -173,6 +173,18 @@ def test_layer_bad_widths_rejected(lib, d_model, q_rank):
     assert lib.sga_layer_workspace_size(ctypes.byref(d), ctypes.byref(lw), sga.LAYER_FORWARD, ctypes.byref(out)) == 1
 
 
+def test_layer_widths_past_2_to_30_rejected(lib):
+    """Near 2^31 a row count of the packed weights would overflow an int, and the workspace size wrap with it."""
+    d = ctypes.byref(sga.make_dims(1, 1, 100))
+    out = ctypes.c_size_t(0)
+    for width in ((1 << 30) + 8, 2**31 - 1024, 2**31 - 8):
+        for bad in (dict(d_model=width), dict(q_rank=width)):
+            lw = _layer_weights(**bad)
+            assert lib.sga_layer_workspace_size(d, ctypes.byref(lw), sga.LAYER_FORWARD, ctypes.byref(out)) == 1, bad
+    lw = _layer_weights(q_rank=1 << 30)
+    assert lib.sga_layer_workspace_size(d, ctypes.byref(lw), sga.LAYER_FORWARD, ctypes.byref(out)) == 0
+
+
 def test_layer_bad_arguments_rejected_on_host(lib):
     d = sga.make_dims(2, 1, 1000)
     P = ctypes.c_void_p
