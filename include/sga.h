@@ -278,7 +278,8 @@ SGA_API sga_status_t sga_forward_kv4(const sga_dims_t* dims, const sga_bf16_t* q
  * as the largest bf16 and becomes +-448; a NaN stays a NaN and does not count.
  *   x [rows][cols] bf16    codes [rows][cols] E4M3 bytes
  *   scale [rows][ceil(cols / 128)] fp32
- * cols is a multiple of 16, at most 2^30; x and codes 16-byte aligned. */
+ * cols is a multiple of 16, at most 2^30, and there are at most 2^30 scales; x
+ * and codes 16-byte aligned. */
 SGA_API sga_status_t sga_quantize_fp8(int32_t rows, int32_t cols, const sga_bf16_t* x, sga_fp8_e4m3_t* codes,
                                       float* scale, sga_stream_t stream);
 

@@ -1101,7 +1101,7 @@ cudaError_t launch_tile(const GemmFp8Args& a, int num_sms, cudaStream_t s) {
 cudaError_t launch_quantize_fp8(int rows, int cols, const uint16_t* x, uint8_t* codes, float* scale, cudaStream_t s) {
   const int col_blocks = (cols + kBlock - 1) / kBlock;
   const long long blocks = static_cast<long long>(rows) * col_blocks;
-  if (blocks > INT32_MAX / 2) return cudaErrorInvalidValue;  // over 256 GB of activations
+  if (blocks > kMaxExtent) return cudaErrorInvalidValue;
   constexpr int per = 256 / kQuantLanes;
   const int n = static_cast<int>(blocks);
   if (n <= 148 * 8 * per)  // one wave
@@ -1136,6 +1136,7 @@ sga_status_t sga_quantize_fp8(int32_t rows, int32_t cols, const sga_bf16_t* x, s
                               sga_stream_t stream) {
   using sga::host::aligned;
   if (rows < 1 || cols < 16 || cols % 16 != 0 || cols > sga::kMaxExtent) return SGA_ERR_INVALID_ARG;
+  if (static_cast<long long>(rows) * ((cols + sga::kBlock - 1) / sga::kBlock) > sga::kMaxExtent) return SGA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return SGA_ERR_INVALID_ARG;
   int sms = 0;
   const sga_status_t st = sga::host::device_info(&sms);

@@ -130,6 +130,11 @@ def test_quantize_refuses_bad_arguments(lib):
     assert lib.sga_quantize_fp8(1, 16, GOOD, GOOD, ODD, None) == 1
 
 
+@pytest.mark.parametrize("rows,cols", [(2**30 + 1, 16), (2**31 - 1, 128), (2**29 + 1, 144), (2**20, 2**18)])
+def test_quantize_refuses_more_than_2_to_30_scales(lib, rows, cols):
+    assert lib.sga_quantize_fp8(rows, cols, GOOD, GOOD, GOOD, None) == 1
+
+
 def test_product_refuses_bad_arguments(lib):
     def call(n=4, m=5, k=32, x=GOOD, xs=GOOD, w=GOOD, wsc=GOOD, y=GOOD, t=0, ws=WS, nbytes=256):
         return lib.sga_gemm_fp8(n, m, k, x, xs, w, wsc, y, t, ws, nbytes, None)
