@@ -247,8 +247,11 @@ SGA_API sga_status_t sga_kv4_read(const sga_dims_t* dims, const uint8_t* kv4, co
  *   gate [B][T][64] bf16 or NULL     out [B][T][64][512] bf16 (output; 16-byte
  *        aligned)
  * The contractions accumulate in fp32; the softmax weights are rounded to fp16
- * for the second one.  Within a head, query latent values below 2^-31 of the
- * head's largest one lose low bits.  A query with no valid slot gets zeros.
+ * for the second one.  A head's queries are scaled by a power of two, its largest
+ * value (latent or rope) to between 2^14 and 2^15: latent values below 2^-31 of
+ * that largest one lose low bits, and the selected rows' rope values have to
+ * stay within 2^106 in magnitude (larger ones may overflow the scaled scores).
+ * A query with no valid slot gets zeros.
  * Rows that idx does not name are not read, whatever they hold.  Workspace:
  * 256 bytes.  Device error: an index outside [-1, L) (the slot is treated as
  * empty). */

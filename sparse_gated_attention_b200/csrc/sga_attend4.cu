@@ -18,7 +18,8 @@
 //   * Q must then be fp16 for the latent dims.  Each head is scaled by the power
 //     of two that takes its largest value into [2^14, 2^15): a bf16 value keeps
 //     its 8 bits exactly down to 2^-31 of the head's largest, and the factor
-//     is taken out again in the softmax scale.  The rope dims stay bf16 on both
+//     is taken out again in the softmax scale.  (The scaled scores stay finite
+//     for cache rope values up to 2^106: 64 products below 2^15 * 2^106.)  The rope dims stay bf16 on both
 //     sides (kind::f16 takes either type, one per instruction).
 // Otherwise as there: one CTA per (query, split), the splits of a query a cluster;
 // QK^T with M = 64 heads, N = 64 rows; PV transposed, O^T [512 x 64] in tensor
