@@ -132,11 +132,12 @@ def _quantised(x: np.ndarray) -> np.ndarray:
     return block_scaled(codes, scale, 1).reshape(x.shape)
 
 
-def layer_forward(h, q_pos, packed, k_idx_cache, wts: dict, k: int = 2048, n_threads: int = 0) -> dict:
+def layer_forward(h, q_pos, packed, k_idx_cache, wts: dict, k: int = 2048, n_threads: int = 0, idx=None) -> dict:
     """The layer of sga_layer_forward_fp8kv4 in fp64, every activation between two contractions rounded to bf16.
 
     packed [B,L,416] bytes and k_idx_cache [B,L,128] are updated copies in the result; wts as layer_forward_fp8kv4
-    takes them.  Dense selections only (all positions 0..q_pos within k), where the indexer plays no part."""
+    takes them.  The attention is over `idx` [B,T,k], or over all positions 0..q_pos (at most k); what the indexer scores
+    with (q_idx, w and the keys) is in the result."""
     from . import layer
 
     def weights(name):
@@ -162,11 +163,14 @@ def layer_forward(h, q_pos, packed, k_idx_cache, wts: dict, k: int = 2048, n_thr
     code, scale, rope_v = kv4_pack(kv_row.reshape(B * T, -1))
     bits = layer.bf16_bits(rope_v).view(np.uint8).reshape(B * T, 128)
     rows = np.concatenate([code[:, 0::2] | (code[:, 1::2] << 4), scale, bits], 1).reshape(B, T, ROW_BYTES)
-    idx = np.full((B, T, k), -1, dtype=np.int32)
+    dense = np.full((B, T, k), -1, dtype=np.int32)
     for b in range(B):
         for t in range(T):
             packed[b, pos[b, t]], k_idx[b, pos[b, t]] = rows[b, t], k_row[b, t]
-            idx[b, t, :pos[b, t] + 1] = np.arange(pos[b, t] + 1)
+            if idx is None:
+                dense[b, t, :pos[b, t] + 1] = np.arange(pos[b, t] + 1)
+    idx = dense if idx is None else idx
     out = rb(attend_kv4(q, packed, idx, gate)[0])
     o = rb(np.einsum("bthj,hij->bthi", out, to_f64(wts["w_uv"]))).reshape(B, T, -1)
-    return {"idx": idx, "packed": packed, "k_idx": k_idx, "y": _quantised(o) @ w_o.T}
+    return {"idx": idx, "packed": packed, "k_idx": k_idx, "y": _quantised(o) @ w_o.T,
+            "q_idx": rb(g2[..., 12416:]).reshape(B, T, 64, 128), "w": rb(g1[..., rp + 768:])}

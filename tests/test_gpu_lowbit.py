@@ -152,6 +152,14 @@ def test_product_matches_definition(n, m, k, out_dtype):
     check_product(n, m, k, out_dtype, seed=n + m + k)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,m,k", [(500, 7168, 8192), (700, 4098, 7184), (1100, 2049, 1552), (1153, 20608, 1536),
+                                   (1000, 4608, 912)])
+def test_product_of_many_tokens_at_depths_in_use(n, m, k, out_dtype):
+    """Tiles of 256 x 256 (by a margin in the rule that chooses), K of 8 to 64 blocks, the last one whole or partial."""
+    check_product(n, m, k, out_dtype, seed=n + m + k)
+
+
 @pytest.mark.parametrize("n", [9, 30, 50, 100])
 @pytest.mark.parametrize("m,units", [(77, 2), (77, 6), (77, 7), (77, 9), (77, 10), (77, 11), (77, 13), (77, 17), (77, 21),
                                      (77, 31), (5800, 6), (5800, 8)])
@@ -473,6 +481,41 @@ def test_attend_kv4_nan_in_a_selected_row_shows():
     assert bool(torch.isnan(sga.sparse_mla_attend_kv4(q, cache, idx)).all())
 
 
+def test_attend_kv4_infinite_and_nan_queries_stay_in_their_heads():
+    """A NaN or an infinity in a head, in the latent or the rope dims, makes that head's output NaN and no other's."""
+    g = gen(16)
+    cache = fill_cache(g, 1, 400)
+    q = randn(g, 1, 3, 64, 576).to(torch.bfloat16)
+    idx = pick(g, 1, 3, 400, 384)
+    want = sga.sparse_mla_attend_kv4(q, cache, idx)
+    bad = q.clone()
+    for head, dim, value in ((3, 100, "nan"), (17, 570, "nan"), (40, 0, "inf"), (41, 575, "-inf"), (63, 511, "inf")):
+        bad[0, 1, head, dim] = float(value)
+    got = sga.sparse_mla_attend_kv4(bad, cache, idx)
+    hit = torch.zeros((1, 3, 64), dtype=torch.bool, device=DEV)
+    hit[0, 1, [3, 17, 40, 41, 63]] = True
+    assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[~hit], want[~hit])
+
+
+def test_attend_kv4_rope_values_over_their_range():
+    """Cache rope values up to 2^106 in magnitude, against queries of 2^-103 and of 1 in the rope dims."""
+    g = gen(17)
+    rows = randn(g, 1, 128, 576)
+    rows[..., 512:] = rows[..., 512:].clamp(-4, 4) * 2.0 ** 104
+    idx = torch.arange(128, dtype=torch.int32, device=DEV).view(1, 1, 128).contiguous()
+    cache = torch.zeros((1, 128, 416), dtype=torch.uint8, device=DEV)
+    sga.kv4_append(rows.to(torch.bfloat16), idx[0], cache)
+    q = randn(g, 1, 1, 64, 576)
+    small = q * 2.0 ** -103
+    check_attend(small.to(torch.bfloat16), cache, idx, None)
+    q[..., 512:] = torch.where(torch.arange(64, device=DEV)[:, None] == torch.arange(64, device=DEV), 1.0, 0.0)
+    # one rope dim a head: its largest cache value takes all the weight
+    got = sga.sparse_mla_attend_kv4(q.to(torch.bfloat16), cache, idx)
+    values = torch.tensor(lowbit.kv4_values(cache[0].cpu().numpy()), device=DEV)
+    best = values[:, 512:].argmax(0)
+    assert torch.equal(got[0, 0].double(), values[best, :512])
+
+
 def test_attend_kv4_index_out_of_range_is_reported_and_left_out():
     g = gen(12)
     cache = fill_cache(g, 2, 50)
@@ -664,6 +707,44 @@ def test_layer_fp8kv4_matches_definition(D, R, B, T, L, pos):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(idx3, idx) and torch.equal(y3, y)
+
+
+@pytest.mark.parametrize("D,R,B,T,L,K,first", [(1040, 400, 2, 3, 300, 64, 250), (512, 144, 1, 12, 700, 128, 500),
+                                               (7168, 1536, 3, 1, 3000, 2048, 2900)])
+def test_layer_fp8kv4_selects_by_its_own_index_queries(D, R, B, T, L, K, first):
+    """Fewer slots than positions, so the indices depend on q_idx, w and the keys (R with and without whole blocks of
+    128).  They are compared with the definition's scores in 64 bits, up to a band around the K-th: an activation next
+    to a rounding border may change one of its E4M3 codes by a step of 2^-3, which moves the index queries by about
+    2^-3 / sqrt(R) of their size (1e-2 at R = 144), and the scores no more; the band is 1e-2 of the largest score.  y is
+    compared with the definition over the indices that the layer chose."""
+    import oracle
+    from oracle import layer as layer_oracle
+
+    oracle.build()
+    wts = fp8_layer_weights(D, R, seed=D + 7)
+    g = gen(D + 3)
+    h = randn(g, B, T, D).to(torch.bfloat16)
+    q_pos = torch.stack([torch.arange(T, device=DEV) + first + 5 * b for b in range(B)]).to(torch.int32)
+    cache, k_idx = fill_cache(g, B, L), randn(g, B, L, 128).to(torch.bfloat16)
+    cache0, k_idx0 = cache.clone(), k_idx.clone()
+    ws = sga.alloc_layer_fp8kv4_workspace(sga.make_dims(B, T, L, K), sga.layer_fp8_weights(wts))
+    idx, y = sga.layer_forward_fp8kv4(wts, h, q_pos, cache, k_idx, top_k=K, ws=ws)
+    assert sga.device_status(ws) == 0
+    got = idx.cpu().numpy()
+    want = lowbit.layer_forward(h, q_pos, cache0, k_idx0, wts, k=K, idx=got)
+    scores = oracle.index_scores(layer_oracle.bf16_bits(want["q_idx"]), layer_oracle.bf16_bits(want["w"]),
+                                 layer_oracle.bf16_bits(want["k_idx"]), q_pos.cpu())
+    for b in range(B):
+        for t in range(T):
+            p = int(q_pos[b, t])
+            s, sel = scores[b, t, :p + 1], got[b, t]
+            assert (sel >= 0).all() and (sel <= p).all() and (np.diff(sel) > 0).all()
+            kth, band = np.sort(s)[-K], 1e-2 * np.abs(s).max()
+            chosen = np.zeros(p + 1, dtype=bool)
+            chosen[sel] = True
+            assert s[chosen].min() >= kth - band and s[~chosen].max() <= kth + band, (b, t)
+    rel = np.linalg.norm(lowbit.to_f64(y) - want["y"]) / np.linalg.norm(want["y"])
+    assert rel <= 1e-2, f"rel-L2 {rel:.3e}"
 
 
 def test_layer_fp8kv4_position_out_of_range_is_reported():
