@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
     // indices are fetched one iteration before that.
     auto load_idx = [&](int j) {
       // K is a multiple of 64: a chunk has no tail
+      SGA_DCHECK(p.status, j >= nchunks || (slot_base >= 0 && slot_base + j * kChunk + r < p.top_k));
       return j < nchunks ? __ldg(idx_row + slot_base + j * kChunk + r) : -1;
     };
     auto load = [&](RowPart& d, int v) {
@@ -750,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) sga_attend4_kernel(Attend4Params 
           const int v = dim >> 2;
           const int owner = ((v + 1) * S - 1) / (kDv / 4);  // the r with v0(r) <= v < v0(r + 1)
           const int dl = dim - 4 * ((kDv / 4) * owner / S);
+          SGA_DCHECK(p.status, owner < S && dl >= 0 && dl < kStride);
           float* col = cluster.map_shared_rank(recv + (split * kHeads + c * 32) * kStride + dl, owner);
 #pragma unroll
           for (int i = 0; i < 32; ++i) col[i * kStride] = o[i];

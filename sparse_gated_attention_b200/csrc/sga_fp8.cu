@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
       bool ok = true;
       for (int t = first; t < p.tiles && ok; t += step) {
         const int row0 = t / p.n_blocks * kTileM, token0 = t % p.n_blocks * NP;
+        SGA_DCHECK(p.status, row0 < p.m && token0 < p.n && u0 < u1 && u1 <= p.units);
         for (int u = u0; u < u1; ++u, ++n_done) {
           if (n_done >= pre) {
             if (!mbar_wait(empty(st), ph ^ 1u, abort_flag)) {
@@ -577,6 +578,7 @@ __global__ void __launch_bounds__(StreamCfg<NP>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {
         const int c = col0 + i, r = ((c + 1) * S - 1) / NP;  // the r with c0(r) <= c < c0(r + 1)
+        SGA_DCHECK(p.status, r < S && c0_of(r) <= c && c < c0_of(r + 1) && c - c0_of(r) < width);
         st_cluster(map_to_rank(mine + 4u * (c - c0_of(r)) * kTileM, r), acc[i]);
       }
       cluster_barrier();
@@ -822,6 +824,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         bool ok = true;
         for (int t = pair; t < p.tiles && ok; t += pairs) {
           const int tn = t % p.n_tiles, tm = t / p.n_tiles;
+          SGA_DCHECK(p.status, 2 * tn * kTM < p.n && tm * kTN < p.m);
           for (int kb = 0; kb < p.k_blocks; ++kb) {
             if (!mbar_wait_idle(empty(st), ph ^ 1u, abort_flag)) {
               ok = false;

@@ -113,3 +113,50 @@ def test_debug_build_runs_clean_and_matches_the_oracle():
                          text=True, timeout=900)
     assert res.returncode == 0, res.stdout[-3000:] + res.stderr[-3000:]
     assert "debug build ok" in res.stdout
+
+
+SCRIPT_FEW_BITS = r"""
+import sys
+sys.path.insert(0, ROOT)
+import numpy as np
+import torch
+import sparse_gated_attention_b200 as sga
+from oracle import lowbit
+from tests import test_gpu_lowbit as low
+
+lib = sga.load_library()
+assert lib._name.endswith("libsga_debug.so"), lib._name
+
+# the block-scaled product: unsplit, split in two to eight, tiles of 256 x 256; the quantiser in front of it
+for n, m, k in [(1, 300, 2048), (9, 77, 5008), (30, 5800, 1424), (64, 2304, 7168), (100, 513, 1040), (700, 4098, 4112)]:
+    for dtype in (torch.float32, torch.bfloat16):
+        low.check_product(n, m, k, dtype, seed=n + k)  # its status too
+low.check_quantize(low.randn(low.gen(1), 37, 1552).to(torch.bfloat16))
+
+# the 4-bit cache and the attention over it: whole queries, split ones, empty slots
+pos = torch.tensor([[5, 0, 3], [1, 2, 39]], dtype=torch.int32, device="cuda")
+low.check_append(low.randn(low.gen(2), 2, 3, 576).to(torch.bfloat16), pos, 40)
+for B, T, L, K, fill in [(1, 1, 64, 64, 1.0), (3, 1, 3000, 2048, 1.0), (2, 5, 1001, 1088, 0.9), (1, 150, 400, 128, 1.0)]:
+    g = low.gen(B + T)
+    cache = low.fill_cache(g, B, L)
+    q = low.randn(g, B, T, 64, 576).to(torch.bfloat16)
+    low.check_attend(q, cache, low.pick(g, B, T, L, K, fill), low.randn(g, B, T, 64).to(torch.bfloat16))
+
+# the layer on both, a decode step and a short prompt
+low.test_layer_fp8kv4_matches_definition(1040, 400, 2, 3, 300, [[0, 5, 299], [100, 101, 102]])
+low.test_layer_fp8kv4_selects_by_its_own_index_queries(512, 144, 1, 12, 700, 128, 500)
+print("debug build in few bits ok")
+"""
+
+
+def test_debug_build_in_few_bits_runs_clean_and_matches_the_definitions():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_gated_attention_b200 import build
+
+    build.build(debug=True)
+    env = dict(os.environ, SGA_LIBRARY="debug")
+    res = subprocess.run([sys.executable, "-c", SCRIPT_FEW_BITS.replace("ROOT", repr(ROOT))], env=env,
+                         capture_output=True, text=True, timeout=900)
+    assert res.returncode == 0, res.stdout[-3000:] + res.stderr[-3000:]
+    assert "debug build in few bits ok" in res.stdout
