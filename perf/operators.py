@@ -24,7 +24,7 @@ SCALE = 192.0 ** -0.5
 BLOCK = 128
 GROUP = 16
 MAX_WORK_ROWS = 512  # queries of the largest prefill block measured
-STATUS_WS, PRODUCT_WS = 256, 24 << 20  # bytes of the zero-filled workspace that a program keeps for the calls
+STATUS_WS = 256  # bytes of the zero-filled workspace that a program keeps for the calls
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 OUT_TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
 
@@ -86,7 +86,7 @@ def draw(rng):
 def prepare(case, seed):
     g = torch.Generator(device="cuda")
     g.manual_seed(int(seed))
-    ws = torch.zeros(PRODUCT_WS if case["op"] == "product" else STATUS_WS, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(STATUS_WS, dtype=torch.uint8, device="cuda")
     make = {"quantize": _prepare_quantize, "product": _prepare_product, "cache": _prepare_cache,
             "attend": _prepare_attend}[case["op"]]
     return {"case": dict(case), "ws": ws, **make(case, g)}
