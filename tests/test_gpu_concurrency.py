@@ -176,3 +176,20 @@ def test_what_a_call_makes_belongs_to_the_given_stream(calls, name):
             assert float((a - b).norm()) <= 1e-3 * float(b.norm())
         else:
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_a_stream_of_another_library(calls):
+    """Any object with a cuda_stream names a stream."""
+    class Foreign:
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    s = torch.cuda.Stream()
+    for name in ("forward", "forward_kv4", "gemm_fp8", "quantize_fp8"):
+        with torch.cuda.stream(s):
+            want = _copies(calls[name](s))
+        s.synchronize()
+        got = calls[name](Foreign(s))
+        s.synchronize()
+        for a, b in zip(_copies(got), want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
