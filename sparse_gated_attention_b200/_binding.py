@@ -174,6 +174,11 @@ def _strides(shape) -> tuple:
     return tuple(reversed(strides))
 
 
+def _other(stream):
+    """Whether `stream` is given and is not the current one (making it that costs some 5 us)."""
+    return stream is not None and stream.cuda_stream != _stream(None)
+
+
 def _on(stream):
     """`stream` (any object with a cuda_stream) as the current stream."""
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
@@ -183,7 +188,7 @@ def _on(stream):
 def _empty(shape, dtype, device, stream=None):
     """A contiguous tensor: torch.empty at half its cost, which counts in a decode step's short calls.  Its memory belongs
     to `stream`, the one that the call launches on: on any other, torch could hand it out while that one still uses it."""
-    if stream is not None:
+    if _other(stream):
         with _on(stream):
             return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
     return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
@@ -191,7 +196,7 @@ def _empty(shape, dtype, device, stream=None):
 
 def _zeros(shape, dtype, device, stream=None):
     """A tensor of zeros, filled on `stream` (its memory belongs to it, see _empty), or on the current one."""
-    if stream is not None:
+    if _other(stream):
         with _on(stream):
             return torch.zeros(shape, dtype=dtype, device=device)
     return torch.zeros(shape, dtype=dtype, device=device)
