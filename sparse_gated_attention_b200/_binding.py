@@ -174,32 +174,30 @@ def _strides(shape) -> tuple:
     return tuple(reversed(strides))
 
 
-def _other(stream):
-    """Whether `stream` is given and is not the current one (making it that costs some 5 us)."""
-    return stream is not None and stream.cuda_stream != _stream(None)
-
-
-def _on(stream):
-    """`stream` (any object with a cuda_stream) as the current stream."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
-                             torch.cuda.ExternalStream(stream.cuda_stream))
+def _on(stream, make, *args, **kwargs):
+    """make(...) with `stream` (any object with a cuda_stream, or None) as the current stream: the memory that it takes
+    belongs to that stream.  torch could hand out any other stream's while this one still uses it."""
+    if stream is None or stream.cuda_stream == _stream(None):
+        return make(*args, **kwargs)
+    here = torch.cuda.current_stream()
+    torch.cuda.set_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                          torch.cuda.ExternalStream(stream.cuda_stream))
+    try:
+        return make(*args, **kwargs)
+    finally:
+        torch.cuda.set_stream(here)
 
 
 def _empty(shape, dtype, device, stream=None):
-    """A contiguous tensor: torch.empty at half its cost, which counts in a decode step's short calls.  Its memory belongs
-    to `stream`, the one that the call launches on: on any other, torch could hand it out while that one still uses it."""
-    if _other(stream):
-        with _on(stream):
-            return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
-    return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
+    """A contiguous tensor on `stream`: torch.empty at half its cost, which counts in a decode step's short calls."""
+    if stream is None:
+        return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=device)
+    return _on(stream, torch.empty_strided, shape, _strides(shape), dtype=dtype, device=device)
 
 
 def _zeros(shape, dtype, device, stream=None):
-    """A tensor of zeros, filled on `stream` (its memory belongs to it, see _empty), or on the current one."""
-    if _other(stream):
-        with _on(stream):
-            return torch.zeros(shape, dtype=dtype, device=device)
-    return torch.zeros(shape, dtype=dtype, device=device)
+    """A tensor of zeros, filled on `stream`, or on the current one."""
+    return _on(stream, torch.zeros, shape, dtype=dtype, device=device)
 
 
 def _one_device(*tensors):
