@@ -45,7 +45,9 @@ constexpr int kBlock = 128;  // K elements (bytes) and weight rows that share a 
 // overflows, or loses bits as a subnormal or zero) v * x_scale * w_scale may still be one: v is zero or between 2^-18
 // and 2^25 in magnitude (E4M3 products are multiples of 2^-18).  Such pairs are rare, and a branch in the accumulating
 // loops costs 3% to 20% of the large products.  So the warps that fetch the scales only note that the thread block met
-// one, and after its last tile it looks for the elements concerned and computes them once more, here.
+// one, and after its last tile it looks for the elements concerned and computes them once more, here.  An infinite
+// product leaves an infinity or a NaN (also on v = 0).  A subnormal one is off by at most 2^-150, so its block by 2^-125:
+// within fp32's rounding of any result from 2^-100 on.
 
 // Zero, subnormal, infinite or NaN.
 __device__ __forceinline__ bool not_normal(float s) {
@@ -80,6 +82,8 @@ __device__ __forceinline__ ScalePair scale_pair(float x, float w) {
   // a rest of 2^128 and more times v is infinite for every v but zero, and so is FLT_MAX
   return {copysignf(fminf(big * 0x1p-100f * small, FLT_MAX), s), 0x1p100f};
 }
+
+__device__ __forceinline__ bool sure(float y) { return fabsf(y) >= 0x1p-100f && fabsf(y) <= FLT_MAX; }
 
 __device__ __noinline__ bool any_odd_pair(const float* xs, const float* ws, int k_blocks) {
   bool odd = false;
@@ -247,6 +251,13 @@ __device__ __forceinline__ void store_y(const StreamParams& p, int row, int toke
   }
 }
 
+// y[token][row] as it was stored.
+template <class Params>
+__device__ __forceinline__ float load_y(const Params& p, int token, int row) {
+  const size_t at = static_cast<size_t>(token) * p.m + row;
+  return p.out_bf16 ? __uint_as_float(static_cast<uint32_t>(p.out_bf16[at]) << 16) : p.out_f32[at];
+}
+
 // Computes this thread's outputs of every tile of its thread block once more where a block's scales have no normal
 // product.  (By itself, so that nothing of it is held in registers meanwhile.)
 template <int NP>
@@ -262,6 +273,7 @@ __device__ __noinline__ void redo_stream_tiles(StreamParams p) {
     if (row >= p.m) continue;
     const float* ws = p.w_scale + static_cast<size_t>(row / kBlock) * p.k_blocks;
     for (int i = token0 + c0; i < min(token0 + c1, p.n); i += p.splits == 1 ? 1 : Cfg::kGroups) {
+      if (sure(load_y(p, i, row))) continue;
       const float* xs = p.x_scale + static_cast<size_t>(i) * p.k_blocks;
       if (!any_odd_pair(xs, ws, p.k_blocks)) continue;
       const float y = scaled_dot(p.x + static_cast<size_t>(i) * p.k, p.w + static_cast<size_t>(row) * p.k, xs, ws, p.k);
@@ -734,23 +746,24 @@ __device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float
       : "f"(x), "f"(y), "f"(s));
 }
 
-// As redo_stream_tiles: a thread takes a token's channels of one block of weight rows.
+// As redo_stream_tiles: a warp takes its 32 tokens one by one, a lane every 32nd of its 128 channels.
 __device__ __noinline__ void redo_tiles(TileParams p) {
-  const int warp = threadIdx.x >> 5, tok = (warp & 3) * 32 + (threadIdx.x & 31), half = (warp - 4) >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, half = (warp - 4) >> 2;
   for (int t = blockIdx.x >> 1; t < p.tiles; t += gridDim.x >> 1) {
-    const int token = (2 * (t % p.n_tiles) + (blockIdx.x & 1)) * kTM + tok, ch0 = t / p.n_tiles * kTN + half * kBlock;
-    if (token >= p.n || ch0 >= p.m) continue;
-    const float* xs = p.x_scale + static_cast<size_t>(token) * p.k_blocks;
+    const int token0 = (2 * (t % p.n_tiles) + (blockIdx.x & 1)) * kTM + quarter * 32;
+    const int ch0 = t / p.n_tiles * kTN + half * kBlock;
     const float* ws = p.w_scale + static_cast<size_t>(ch0 / kBlock) * p.k_blocks;
-    if (!any_odd_pair(xs, ws, p.k_blocks)) continue;
-    const uint8_t* x = p.x + static_cast<size_t>(token) * p.k;
-    for (int ch = ch0; ch < min(ch0 + kBlock, p.m); ++ch) {
-      const float y = scaled_dot(x, p.w + static_cast<size_t>(ch) * p.k, xs, ws, p.k);
-      const size_t at = static_cast<size_t>(token) * p.m + ch;
-      if (p.out_bf16) {
-        p.out_bf16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-      } else {
-        p.out_f32[at] = y;
+    for (int token = token0; token < min(token0 + 32, p.n); ++token) {
+      const float* xs = p.x_scale + static_cast<size_t>(token) * p.k_blocks;
+      for (int ch = ch0 + lane; ch < min(ch0 + kBlock, p.m); ch += 32) {
+        if (sure(load_y(p, token, ch)) || !any_odd_pair(xs, ws, p.k_blocks)) continue;
+        const float y = scaled_dot(p.x + static_cast<size_t>(token) * p.k, p.w + static_cast<size_t>(ch) * p.k, xs, ws, p.k);
+        const size_t at = static_cast<size_t>(token) * p.m + ch;
+        if (p.out_bf16) {
+          p.out_bf16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        } else {
+          p.out_f32[at] = y;
+        }
       }
     }
   }

@@ -257,6 +257,39 @@ def test_product_scales_over_the_whole_range(n, m, k, out_dtype):
     assert int(big.sum()) > 0 and int((finite & (want > 0)).sum()) > 0
 
 
+@pytest.mark.parametrize("n,m,k", [(7, 260, 400), (60, 260, 1680), (100, 260, 2064), (1100, 2050, 528)])
+def test_product_extreme_scales_beside_ordinary_ones(n, m, k):
+    """Tokens whose blocks have scales of 2^-140 .. 2^-100, 2^120 and ordinary ones side by side, with values of both
+    signs; where the scale is 2^120 the codes are zero in two tokens of three.  The weight scales are ordinary but for
+    every fourth block's, 2^-30 or 2^30.  A block's error is at most (128 + 2) 2^-23 of its own size."""
+    x, xs, w, wsc = product_case(n, m, k, n)
+    g = gen(k)
+    kb = xs.shape[1]
+    pick_one = torch.randint(0, 6, (n, kb), generator=g, device=DEV)
+    xs = torch.where(pick_one == 0, torch.exp2(torch.randint(-140, -99, (n, kb), generator=g, device=DEV).float()), xs)
+    xs = torch.where(pick_one == 1, 2.0 ** 120, xs)
+    xs[3] = torch.exp2(torch.randint(-140, -99, (kb,), generator=g, device=DEV).float())  # small throughout
+    pick_one[3] = 0
+    huge = (pick_one == 1) & (torch.arange(n, device=DEV) % 3 != 0)[:, None]
+    x = torch.where(huge.repeat_interleave(128, 1)[:, :k], 0, x.to(torch.int32)).to(torch.uint8)
+    wsc[:, 0::4] = 2.0 ** -30
+    wsc[:, 1::4] = 2.0 ** 30
+    y = sga.gemm_fp8(x, xs, w, wsc).double()
+    X = torch.tensor(lowbit.E4M3[x.cpu().numpy()], device=DEV)
+    W = torch.tensor(lowbit.E4M3[w.cpu().numpy()], device=DEV)
+    want, size = torch.zeros_like(y), torch.zeros_like(y)
+    for j in range(kb):
+        part = slice(128 * j, 128 * j + 128)
+        s = xs[:, j, None].double() * wsc[:, j].double().repeat_interleave(128)[:m]
+        want += X[:, part] @ W[:, part].T * s
+        size += X[:, part].abs() @ W[:, part].T.abs() * s
+    tol = (k + 2 * kb + 2) * 2.0 ** -23 * size + (kb + 1) * 2.0 ** -149
+    # a partial sum past the largest fp32 value may meet its opposite: such elements are not compared
+    fits = size < 2.0 ** 127
+    assert float(fits.double().mean()) > 0.3 and bool(fits[3].all())
+    assert bool(((y - want).abs() <= tol)[fits].all())
+
+
 def test_product_leading_dims_and_out():
     x, xs, w, wsc = product_case(6, 96, 256, 5)
     want = sga.gemm_fp8(x, xs, w, wsc, out_dtype=torch.bfloat16)
