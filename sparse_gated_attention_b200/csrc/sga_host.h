@@ -13,8 +13,9 @@ namespace sga {
 namespace host {
 
 constexpr size_t kWsAlign = 256;      // every workspace region starts on this boundary
-// Clusters of 1 .. 8 thread blocks (one per SM) that a B200 holds at a time: its SMs are in groups of unequal size, which
-// clusters do not cross.
+// Clusters of 1 .. 8 thread blocks (one per SM) that the B200 measured held at a time: its SMs are in groups of unequal
+// size, which clusters do not cross.  Another one's groups may differ: the splits chosen by these counts are then right,
+// and a little slower.
 constexpr int kClusters[8] = {148, 74, 45, 33, 26, 22, 15, 15};
 constexpr size_t kStatusBytes = 256;  // the status block at the start of a workspace
 
