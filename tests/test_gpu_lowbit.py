@@ -312,6 +312,31 @@ def test_product_writes_from_any_element_on(n, m, k, out_dtype):
     assert torch.equal(out, want) and room[0] == 7 and room[-1] == 7
 
 
+def test_quantiser_and_product_past_2_to_32_elements():
+    """Activations, codes and an output of more than 2^32 elements each: rows near both ends, and around the 2^32nd
+    element, against the same rows by themselves (the same order of sums, so the same bits)."""
+    g = gen(50)
+    n, m, k = 66_000, 65_600, 144
+    x, xs, w, wsc = product_case(n, m, k, 51)
+    y = sga.gemm_fp8(x, xs, w, wsc, out_dtype=torch.bfloat16)
+    assert y.numel() > 2 ** 32
+    for r in (0, 2 ** 32 // m - 40, n - 80):
+        rows = slice(r, r + 80)
+        assert torch.equal(y[rows], sga.gemm_fp8(x[rows].contiguous(), xs[rows].contiguous(), w, wsc,
+                                                 out_dtype=torch.bfloat16)), r
+    del y
+    rows, cols = 4_000_000, 1088  # 4.35e9
+    a = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV)
+    a.view(torch.int16).fill_(0x3F80)
+    for r in (0, 2 ** 32 // cols - 40, rows - 80):
+        a[r:r + 80] = randn(g, 80, cols)
+    codes, scale = sga.quantize_fp8(a)
+    for r in (0, 2 ** 32 // cols - 40, rows - 80):
+        part_codes, part_scale = sga.quantize_fp8(a[r:r + 80].contiguous())
+        assert torch.equal(codes[r:r + 80].view(torch.uint8), part_codes.view(torch.uint8)), r
+        assert torch.equal(scale[r:r + 80], part_scale), r
+
+
 # ------------------------------------------------------------------------------------------------ 4-bit cache rows
 def check_append(rows, pos, L):
     B, T = pos.shape
